@@ -439,6 +439,119 @@ moe_status moe_ep_split_ids(int32_t n, int32_t E_local, int32_t world, const int
 moe_status moe_gather_rows(int32_t n_dst, int32_t n_src, int64_t row_bytes, const int32_t* map,
                            const void* src, void* dst, int32_t* dev_status, moe_stream_t stream);
 
+/* ---- Around the routed experts: the layer for a few tokens, the linear
+ * product and layer norm. The pages have no counterpart of these entry points;
+ * the few-token layer computes moe_experts_forward's function. ---------------
+ *
+ * moe_experts_forward_few: the whole routed-experts layer for T <= 64 tokens (a
+ * decode step) in two kernels, routing included:
+ *   out bf16 [T, H] = RNE_bf16( residual[t] + shared_MLP(hidden[t])
+ *                               + scale * sum_j w[t,j] * MLP_{e(t,j)}(hidden[t]) )
+ * with MLP_e, the weights' layouts and the shared expert as in
+ * moe_experts_forward (h is rounded to bf16 there too), fp32 sums, no atomics:
+ * the same inputs give the same bits.
+ *   logits fp32 [T, E] non-null: routes first; topk_ids int32 [T, k] and
+ *     topk_weights fp32 [T, k] are outputs (each may be NULL) with
+ *     moe_route_topk's values bit for bit. Every row needs k logits that are not
+ *     NaN (a NaN logit may be picked).
+ *   logits NULL: topk_ids and topk_weights are inputs (both required). An id
+ *     outside [0, E) is skipped and flagged (MOE_DEV_BAD_EXPERT_ID); a token
+ *     that names an expert twice gets the sum of both weights.
+ *   residual bf16 [T, H] or NULL; it may be `out` or `hidden`, and `out` may be
+ *     `hidden`.
+ * The time is the touched experts' weights over the memory rate: above 64 tokens
+ * most experts are touched anyway and moe_experts_forward's tensor tiles win.
+ * Needs padding_M 128 (as the forward), down_fp8 0, T <= 64, else
+ * MOE_ERR_UNSUPPORTED; w_gate_up, w_down, ws_gate_up and ws_down 32-byte aligned,
+ * the rest 16-byte, else MOE_ERR_INVALID_ARG. T == 0 is a no-op. `workspace`
+ * (ws_bytes >= moe_few_workspace_bytes, else MOE_ERR_WORKSPACE) is caller-owned;
+ * its first int32 is this call's device status, written by the call. Calls whose
+ * work may overlap need a workspace each. The second kernel is a programmatic
+ * dependent launch of the first (also as an edge of a captured graph); work
+ * enqueued after the call waits for both. */
+#define MOE_FEW_MAX_TOKENS 64
+size_t moe_few_workspace_bytes(const moe_problem* prob);
+moe_status moe_experts_forward_few(const moe_problem* prob, const void* hidden, const float* logits,
+                                   int32_t* topk_ids, float* topk_weights, const void* w_gate_up,
+                                   const void* w_down, const void* ws_gate_up, const void* ws_down,
+                                   float scale, const void* residual, void* out, void* workspace,
+                                   size_t ws_bytes, moe_stream_t stream);
+
+/* moe_linear: a matrix product with its epilogue,
+ *   z = x W^T + bias,  y = act(z) + residual
+ * x bf16 [M, K], W bf16 [N, K] (row pitches ldx, ldw), bias [N] or NULL (fp32 with
+ * bias_f32, else bf16), residual [M, N] or NULL (pitch ldr; fp32 with res_f32,
+ * else bf16), y [M, N] (pitch ldy; fp32 with y_f32, else bf16, one rounding), and,
+ * where z is not NULL, z bf16 [M, N] (pitch ldz): what moe_linear_backward reads.
+ * Sums and the epilogue are fp32. act: MOE_ACT_GELU is the erf form,
+ * z * Phi(z). Pitches are in elements, 0 = the row's length. Outputs and inputs
+ * do not overlap, but y may be the residual (same pitch and type).
+ * M, N >= 0 (0: no-op), K >= 1, K % 8 == 0, ldx % 8 == 0, ldw % 8 == 0, x and W
+ * 16-byte aligned; y, z, bias and residual need only their type's alignment. Up to
+ * 64 rows run in a kernel that streams the weight, more on tcgen05 tiles.
+ * Errors: MOE_ERR_INVALID_ARG for null, misaligned or negative arguments, a pitch
+ * below its row, a bad act; MOE_ERR_UNSUPPORTED for K % 8, ldx % 8 or ldw % 8 and
+ * for sizes above 2^24; MOE_ERR_WORKSPACE. `workspace` (16-byte aligned) holds the
+ * device status word (its first int32, zeroed by the call; MOE_DEV_TIMEOUT) and
+ * partial sums; calls whose work may overlap need one each.
+ * moe_linear_workspace_bytes returns 0 for a descriptor that moe_linear refuses. */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };
+typedef struct moe_linear_desc {
+  int32_t M, N, K;
+  int32_t act;       /* MOE_ACT_* */
+  int32_t bias_f32;
+  int32_t res_f32;
+  int32_t y_f32;     /* y, and dy of the backward pass */
+  int32_t reserved;  /* 0 */
+  int64_t ldx, ldw, ldr, ldy, ldz;
+} moe_linear_desc;
+size_t moe_linear_workspace_bytes(const moe_linear_desc* desc);
+moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const void* bias,
+                      const void* residual, void* y, void* z, void* workspace, size_t ws_bytes,
+                      moe_stream_t stream);
+
+/* moe_linear_backward: with dz = dy * act'(z),
+ *   dx bf16 [M, K] = dz W,  dw bf16 [N, K] = dz^T x,  dbias fp32 [N] = sum over M of dz
+ * (dense; each may be NULL and is then not computed). The residual's gradient is
+ * dy itself. dy [M, N] has y's type and pitch (ldy); z (bf16, pitch ldz) is
+ * moe_linear's z, needed unless act is MOE_ACT_NONE. dz is an operand of two
+ * bf16 matrix products, so there it is rounded to bf16 once; dbias sums it
+ * unrounded. Sums are fp32, in a fixed order. M == 0 writes zeros into dw and dbias.
+ * Arguments and errors as moe_linear; the descriptor's bias_f32, res_f32 and ldr are
+ * not used, x may be NULL without dw and w without dx. */
+size_t moe_linear_backward_workspace_bytes(const moe_linear_desc* desc);
+moe_status moe_linear_backward(const moe_linear_desc* desc, const void* dy, const void* x,
+                               const void* w, const void* z, void* dx, void* dw, float* dbias,
+                               void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_layer_norm: for each row, m = mean(x), r = 1 / sqrt(mean((x - m)^2) + eps),
+ *   y = (x - m) * r * gamma + beta
+ * x, y [M, H] bf16, or fp32 with x_f32, row pitches ldx, ldy in elements (0 = H);
+ * gamma, beta [H] bf16, or fp32 with w_f32; either may be NULL (1 and 0). mean and
+ * rstd fp32 [M], or NULL, receive m and r. fp32 arithmetic, one rounding of y. y may
+ * be x (same pitch). Any H from 1 to 2^24; pointers need only their type's alignment
+ * (16-byte rows are faster). M == 0 is a no-op.
+ * Errors: MOE_ERR_INVALID_ARG for null or misaligned pointers, M < 0, H < 1, a pitch
+ * below H, eps that is not >= 0; MOE_ERR_UNSUPPORTED for H above 2^24. */
+moe_status moe_layer_norm(int32_t M, int32_t H, int64_t ldx, int64_t ldy, int32_t x_f32,
+                          int32_t w_f32, const void* x, const void* gamma, const void* beta,
+                          float eps, void* y, float* mean, float* rstd, moe_stream_t stream);
+
+/* Its backward pass: with xh = (x - mean) * rstd and g = dy * gamma,
+ *   dx = rstd * (g - mean_row(g) - xh * mean_row(g * xh))
+ *   dgamma fp32 [H] = sum over rows of dy * xh,  dbeta fp32 [H] = sum over rows of dy
+ * dy, x, dx as x and y above (pitches lddy, ldx, lddx); mean and rstd as the forward
+ * pass wrote them. dx, dgamma and dbeta may be NULL; dx may be dy or x (same pitch).
+ * The row sums of the weight gradients go through `workspace` (needed when dgamma or
+ * dbeta is given; 16-byte aligned, moe_layer_norm_backward_workspace_bytes), in a
+ * fixed order. M == 0 writes zeros into dgamma and dbeta. */
+size_t moe_layer_norm_backward_workspace_bytes(int32_t M, int32_t H);
+moe_status moe_layer_norm_backward(int32_t M, int32_t H, int64_t lddy, int64_t ldx, int64_t lddx,
+                                   int32_t x_f32, int32_t w_f32, const void* dy, const void* x,
+                                   const void* gamma, const float* mean, const float* rstd, void* dx,
+                                   float* dgamma, float* dbeta, void* workspace, size_t ws_bytes,
+                                   moe_stream_t stream);
+
 /* Capacity of the library's built-in scratch area used by
  * moe_experts_forward_noalloc: 64 MiB of device memory. */
 #define MOE_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)

@@ -22,9 +22,13 @@ __all__ = [
     "moe_dual_blocks", "moe_quant_dual", "moe_swiglu_quant_dual", "moe_swiglu_backward",
     "moe_ep_split_ids", "moe_gather_rows", "moe_down_gemm_weighted", "moe_combine",
     "moe_experts_forward_noalloc", "moe_noalloc_read_status", "moe_selftest_bounded_wait",
-    "moe_unpermute_f16e", "EXPORTED_SYMBOLS",
+    "moe_unpermute_f16e", "moe_few_workspace_bytes", "moe_experts_forward_few", "LinearDesc",
+    "make_linear_desc", "moe_linear_workspace_bytes", "moe_linear",
+    "moe_linear_backward_workspace_bytes", "moe_linear_backward", "moe_layer_norm",
+    "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward", "EXPORTED_SYMBOLS",
     "MOE_OK", "MOE_EPI_STORE", "MOE_EPI_SWIGLU", "MOE_EPI_SWIGLU_FP8", "MOE_EPI_STORE_F32",
     "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_DEV_BAD_EXPERT_ID", "MOE_DEV_TIMEOUT",
+    "MOE_FEW_MAX_TOKENS", "MOE_ACT_NONE", "MOE_ACT_RELU", "MOE_ACT_SILU", "MOE_ACT_GELU",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +45,8 @@ MOE_TILE_AUTO, MOE_TILE_TOKEN_ROWS, MOE_TILE_WEIGHT_ROWS = 0x00, 0x10, 0x20
 MOE_TILE_WEIGHT_ROWS_PAIR = 0x30
 MOE_A_GATHER = 0x100  # moe_grouped_gemm: A = hidden states, rows gathered through the tables
 MOE_TRANS_PER_BLOCK, MOE_TRANS_PER_TILE = 0, 1
+MOE_FEW_MAX_TOKENS = 64
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU = 0, 1, 2, 3
 
 EXPORTED_SYMBOLS = (
     "moe_get_tables_layout", "moe_workspace_bytes", "moe_route_topk", "moe_route_permute",
@@ -51,6 +57,9 @@ EXPORTED_SYMBOLS = (
     "moe_dual_blocks", "moe_quant_dual", "moe_swiglu_quant_dual", "moe_swiglu_backward",
     "moe_ep_split_ids", "moe_gather_rows", "moe_down_gemm_weighted", "moe_combine",
     "moe_noalloc_read_status", "moe_selftest_bounded_wait", "moe_unpermute_f16e",
+    "moe_few_workspace_bytes", "moe_experts_forward_few", "moe_linear_workspace_bytes",
+    "moe_linear", "moe_linear_backward_workspace_bytes", "moe_linear_backward", "moe_layer_norm",
+    "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward",
 )
 
 
@@ -93,6 +102,25 @@ def make_problem(T, H, F, E, top_k, padding_M=128, score_fn="softmax", renormali
                    int(F_shared))
 
 
+class LinearDesc(ctypes.Structure):
+    """Mirror of ``moe_linear_desc``."""
+    _fields_ = [
+        ("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("act", ctypes.c_int32), ("bias_f32", ctypes.c_int32), ("res_f32", ctypes.c_int32),
+        ("y_f32", ctypes.c_int32), ("reserved", ctypes.c_int32), ("ldx", ctypes.c_int64),
+        ("ldw", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldy", ctypes.c_int64),
+        ("ldz", ctypes.c_int64),
+    ]
+
+
+def make_linear_desc(M, N, K, act="none", bias_f32=False, res_f32=False, y_f32=False, ldx=0, ldw=0,
+                     ldr=0, ldy=0, ldz=0) -> LinearDesc:
+    a = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU,
+         "gelu": MOE_ACT_GELU}.get(act, act)
+    return LinearDesc(int(M), int(N), int(K), int(a), int(bool(bias_f32)), int(bool(res_f32)),
+                      int(bool(y_f32)), 0, int(ldx), int(ldw), int(ldr), int(ldy), int(ldz))
+
+
 _LIB = None
 _P = ctypes.c_void_p
 
@@ -107,6 +135,7 @@ def lib() -> ctypes.CDLL:
             f"{library_path} not found: build it with `python -m moe_routed_expert_top_b200.build`")
     L = ctypes.CDLL(library_path)
     PP = ctypes.POINTER(Problem)
+    PD = ctypes.POINTER(LinearDesc)
     sig = {
         "moe_get_tables_layout": (ctypes.c_int, [PP, ctypes.POINTER(TablesLayout)]),
         "moe_workspace_bytes": (ctypes.c_size_t, [PP]),
@@ -146,6 +175,18 @@ def lib() -> ctypes.CDLL:
                                            _P, _P, _P]),
         "moe_noalloc_read_status": (ctypes.c_int, [_P, _P]),
         "moe_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_int64, _P, _P, _P]),
+        "moe_few_workspace_bytes": (ctypes.c_size_t, [PP]),
+        "moe_experts_forward_few": (ctypes.c_int, [PP] + [_P] * 8 + [ctypes.c_float, _P, _P, _P,
+                                                                     ctypes.c_size_t, _P]),
+        "moe_linear_workspace_bytes": (ctypes.c_size_t, [PD]),
+        "moe_linear": (ctypes.c_int, [PD] + [_P] * 7 + [ctypes.c_size_t, _P]),
+        "moe_linear_backward_workspace_bytes": (ctypes.c_size_t, [PD]),
+        "moe_linear_backward": (ctypes.c_int, [PD] + [_P] * 8 + [ctypes.c_size_t, _P]),
+        "moe_layer_norm": (ctypes.c_int, [ctypes.c_int32] * 2 + [ctypes.c_int64] * 2 +
+                           [ctypes.c_int32] * 2 + [_P] * 3 + [ctypes.c_float] + [_P] * 4),
+        "moe_layer_norm_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 2),
+        "moe_layer_norm_backward": (ctypes.c_int, [ctypes.c_int32] * 2 + [ctypes.c_int64] * 3 +
+                                    [ctypes.c_int32] * 2 + [_P] * 9 + [ctypes.c_size_t, _P]),
         "moe_decode_device_status": (ctypes.c_int, [ctypes.c_int32]),
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "moe_last_cuda_error": (ctypes.c_char_p, []),
@@ -346,6 +387,71 @@ def moe_ep_split_ids(n, E_local, world, ids, rank_ids, local_ids, stream=None):
 def moe_gather_rows(n_dst, n_src, row_bytes, map_, src, dst, dev_status=None, stream=None):
     _check(lib().moe_gather_rows(int(n_dst), int(n_src), int(row_bytes), _ptr(map_), _ptr(src),
                                  _ptr(dst), _ptr(dev_status), _stream(stream)), "moe_gather_rows")
+
+
+def moe_few_workspace_bytes(prob: Problem) -> int:
+    return int(lib().moe_few_workspace_bytes(ctypes.byref(prob)))
+
+
+def moe_experts_forward_few(prob, hidden, logits, topk_ids, topk_weights, w_gate_up, w_down,
+                            ws_gate_up, ws_down, scale, residual, out, workspace, ws_bytes=None,
+                            stream=None):
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().moe_experts_forward_few(ctypes.byref(prob), _ptr(hidden), _ptr(logits),
+                                         _ptr(topk_ids), _ptr(topk_weights), _ptr(w_gate_up),
+                                         _ptr(w_down), _ptr(ws_gate_up), _ptr(ws_down),
+                                         float(scale), _ptr(residual), _ptr(out), _ptr(workspace),
+                                         int(ws_bytes), _stream(stream)),
+           "moe_experts_forward_few")
+
+
+def moe_linear_workspace_bytes(desc: LinearDesc) -> int:
+    return int(lib().moe_linear_workspace_bytes(ctypes.byref(desc)))
+
+
+def moe_linear(desc, x, w, bias, residual, y, z, workspace, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().moe_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
+                            _ptr(y), _ptr(z), _ptr(workspace), int(ws_bytes), _stream(stream)),
+           "moe_linear")
+
+
+def moe_linear_backward_workspace_bytes(desc: LinearDesc) -> int:
+    return int(lib().moe_linear_backward_workspace_bytes(ctypes.byref(desc)))
+
+
+def moe_linear_backward(desc, dy, x, w, z, dx, dw, dbias, workspace, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().moe_linear_backward(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(w), _ptr(z),
+                                     _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(workspace),
+                                     int(ws_bytes), _stream(stream)), "moe_linear_backward")
+
+
+def moe_layer_norm(M, H, ldx, ldy, x_f32, w_f32, x, gamma, beta, eps, y, mean=None, rstd=None,
+                   stream=None):
+    _check(lib().moe_layer_norm(int(M), int(H), int(ldx), int(ldy), int(bool(x_f32)),
+                                int(bool(w_f32)), _ptr(x), _ptr(gamma), _ptr(beta), float(eps),
+                                _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream)),
+           "moe_layer_norm")
+
+
+def moe_layer_norm_backward_workspace_bytes(M, H) -> int:
+    return int(lib().moe_layer_norm_backward_workspace_bytes(int(M), int(H)))
+
+
+def moe_layer_norm_backward(M, H, lddy, ldx, lddx, x_f32, w_f32, dy, x, gamma, mean, rstd, dx,
+                            dgamma, dbeta, workspace=None, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().moe_layer_norm_backward(int(M), int(H), int(lddy), int(ldx), int(lddx),
+                                         int(bool(x_f32)), int(bool(w_f32)), _ptr(dy), _ptr(x),
+                                         _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
+                                         _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+                                         int(ws_bytes), _stream(stream)),
+           "moe_layer_norm_backward")
 
 
 def moe_decode_device_status(dev_status: int) -> int:

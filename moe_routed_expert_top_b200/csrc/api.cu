@@ -166,6 +166,99 @@ WorkspacePlan plan_workspace(const moe_problem* pr) {
   return w;
 }
 
+// Whether p (null allowed) is a multiple of `a` bytes.
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// What the few-token layer asks beyond check_problem(prob, true).
+moe_status check_few(const moe_problem* pr) {
+  if (pr->T > moe::kFewMaxTokens || pr->down_fp8) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct FewPlan {
+  int64_t h = 0, hs = 0, total = 0;
+};
+
+FewPlan plan_few(const moe_problem* pr) {
+  FewPlan w;
+  w.h = 1024;  // after the status word
+  w.hs = round_up(w.h + static_cast<int64_t>(pr->T) * pr->top_k * pr->F * 2, 1024);
+  w.total = round_up(w.hs + static_cast<int64_t>(pr->T) * pr->F_shared * 2, 1024);
+  return w;
+}
+
+constexpr int64_t kMaxLinear = 1 << 24;
+
+// A linear descriptor with its pitches filled in.
+struct LinearShape {
+  int M = 0, N = 0, K = 0, y_f32 = 0;
+  int64_t ldx = 0, ldw = 0, ldr = 0, ldy = 0, ldz = 0;
+};
+
+moe_status check_linear(const moe_linear_desc* d, LinearShape* out) {
+  if (d == nullptr) return MOE_ERR_INVALID_ARG;
+  if (d->M < 0 || d->N < 0 || d->K < 1 || d->act < MOE_ACT_NONE || d->act > MOE_ACT_GELU ||
+      d->reserved != 0)
+    return MOE_ERR_INVALID_ARG;
+  LinearShape s;
+  s.M = d->M;
+  s.N = d->N;
+  s.K = d->K;
+  s.y_f32 = d->y_f32 != 0;
+  s.ldx = d->ldx != 0 ? d->ldx : d->K;
+  s.ldw = d->ldw != 0 ? d->ldw : d->K;
+  s.ldr = d->ldr != 0 ? d->ldr : d->N;
+  s.ldy = d->ldy != 0 ? d->ldy : d->N;
+  s.ldz = d->ldz != 0 ? d->ldz : d->N;
+  if (s.ldx < s.K || s.ldw < s.K || s.ldr < s.N || s.ldy < s.N || s.ldz < s.N)
+    return MOE_ERR_INVALID_ARG;
+  if (d->M > kMaxLinear || d->N > kMaxLinear || d->K > kMaxLinear) return MOE_ERR_UNSUPPORTED;
+  if (s.K % 8 != 0 || s.ldx % 8 != 0 || s.ldw % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  // a tensor map's row pitch is below 2^40 bytes
+  const int64_t most = int64_t{1} << 38;
+  if (s.ldx > most || s.ldw > most || s.ldr > most || s.ldy > most || s.ldz > most)
+    return MOE_ERR_UNSUPPORTED;
+  *out = s;
+  return MOE_OK;
+}
+
+int64_t linear_forward_bytes(const LinearShape& d) {
+  if (d.M <= moe::kLinearFewRows) return 1024;
+  return 1024 + 4 * moe::linear_gemm_partial(d.M, d.N, d.K, d.y_f32);
+}
+
+struct LinearBackwardPlan {
+  int64_t dz = 0, lines = 0, partial = 0, total = 0;
+};
+
+LinearBackwardPlan plan_linear_backward(const LinearShape& d) {
+  LinearBackwardPlan b;
+  b.dz = 1024;  // after the status word
+  b.lines = round_up(b.dz + static_cast<int64_t>(d.M) * round_up(d.N, 8) * 2, 1024);
+  b.partial = round_up(
+      b.lines + static_cast<int64_t>(moe::linear_dz_lines(d.M)) * d.N * 4, 1024);
+  // dx and dw follow one another on the stream and share the partial sums' room
+  const int64_t px = d.N > 0 ? moe::linear_gemm_partial(d.M, d.K, d.N, 0) : 0;
+  const int64_t pw = d.M > 0 ? moe::linear_gemm_partial(d.N, d.K, d.M, 0) : 0;
+  b.total = round_up(b.partial + 4 * (px > pw ? px : pw), 1024);
+  return b;
+}
+
+moe_status check_norm(int32_t M, int32_t H, int64_t* a, int64_t* b, int64_t* c) {
+  if (M < 0 || H < 1) return MOE_ERR_INVALID_ARG;
+  for (int64_t* ld : {a, b, c}) {
+    if (ld == nullptr) continue;
+    if (*ld == 0) *ld = H;
+    if (*ld < H) return MOE_ERR_INVALID_ARG;
+  }
+  if (H > kMaxLinear) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int64_t norm_backward_bytes(int32_t M, int32_t H) {
+  return round_up(static_cast<int64_t>(moe::norm_partial_rows(M, H)) * H * 8, 1024);
+}
+
 }  // namespace
 
 extern "C" {
@@ -807,6 +900,295 @@ moe_status moe_gather_rows(int32_t n_dst, int32_t n_src, int64_t row_bytes, cons
     return MOE_ERR_INVALID_ARG;
   MOE_CUDA_TRY(moe::launch_gather_rows_any(n_dst, n_src, row_bytes, map, src, dst, dev_status,
                                            reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+// ---------------------------------------------------------------------------
+// The layer for a few tokens, the linear product and layer norm
+// ---------------------------------------------------------------------------
+
+size_t moe_few_workspace_bytes(const moe_problem* prob) {
+  if (check_problem(prob, true) != MOE_OK || check_few(prob) != MOE_OK) return 0;
+  return static_cast<size_t>(plan_few(prob).total);
+}
+
+moe_status moe_experts_forward_few(const moe_problem* prob, const void* hidden, const float* logits,
+                                   int32_t* topk_ids, float* topk_weights, const void* w_gate_up,
+                                   const void* w_down, const void* ws_gate_up, const void* ws_down,
+                                   float scale, const void* residual, void* out, void* workspace,
+                                   size_t ws_bytes, moe_stream_t stream) {
+  moe_status s = check_problem(prob, true);
+  if (s != MOE_OK) return s;
+  s = check_few(prob);
+  if (s != MOE_OK) return s;
+  if (prob->T == 0) return MOE_OK;
+  if (hidden == nullptr || w_gate_up == nullptr || w_down == nullptr || out == nullptr ||
+      workspace == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (logits == nullptr && (topk_ids == nullptr || topk_weights == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (prob->F_shared > 0 && (ws_gate_up == nullptr || ws_down == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(hidden, 16) || !aligned(w_gate_up, 32) || !aligned(w_down, 32) ||
+      !aligned(ws_gate_up, 32) || !aligned(ws_down, 32) || !aligned(out, 16) ||
+      !aligned(residual, 16) || !aligned(workspace, 16) || !aligned(logits, 4) ||
+      !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
+    return MOE_ERR_INVALID_ARG;
+  const FewPlan w = plan_few(prob);
+  if (ws_bytes < static_cast<size_t>(w.total)) return MOE_ERR_WORKSPACE;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  moe::FewLaunch f;
+  f.T = prob->T;
+  f.H = prob->H;
+  f.F = prob->F;
+  f.E = prob->E;
+  f.k = prob->top_k;
+  f.F_shared = prob->F_shared;
+  f.score_fn = prob->score_fn;
+  f.renormalize = prob->renormalize;
+  f.scale = scale;
+  f.logits = logits;
+  f.topk_ids = topk_ids;
+  f.topk_weights = topk_weights;
+  f.hidden = hidden;
+  f.w_gate_up = w_gate_up;
+  f.w_down = w_down;
+  f.ws_gate_up = ws_gate_up;
+  f.ws_down = ws_down;
+  f.residual = residual;
+  f.h = base + w.h;
+  f.hs = base + w.hs;
+  f.out = out;
+  f.status = reinterpret_cast<int32_t*>(base);
+  MOE_CUDA_TRY(moe::launch_few(f, reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_linear_workspace_bytes(const moe_linear_desc* desc) {
+  LinearShape d;
+  if (check_linear(desc, &d) != MOE_OK) return 0;
+  return static_cast<size_t>(linear_forward_bytes(d));
+}
+
+moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const void* bias,
+                      const void* residual, void* y, void* z, void* workspace, size_t ws_bytes,
+                      moe_stream_t stream) {
+  LinearShape d;
+  moe_status s = check_linear(desc, &d);
+  if (s != MOE_OK) return s;
+  if (d.M == 0 || d.N == 0) return MOE_OK;
+  if (x == nullptr || w == nullptr || y == nullptr || workspace == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(workspace, 16) ||
+      !aligned(bias, desc->bias_f32 ? 4 : 2) || !aligned(residual, desc->res_f32 ? 4 : 2) ||
+      !aligned(y, desc->y_f32 ? 4 : 2) || !aligned(z, 2))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < static_cast<size_t>(linear_forward_bytes(d))) return MOE_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  moe::LinearLaunch g;
+  g.M = d.M;
+  g.N = d.N;
+  g.K = d.K;
+  g.A = x;
+  g.B = w;
+  g.lda = d.ldx;
+  g.ldb = d.ldw;
+  g.e.act = desc->act;
+  g.e.bias_f32 = desc->bias_f32;
+  g.e.res_f32 = desc->res_f32;
+  g.e.y_f32 = desc->y_f32;
+  g.e.bias = bias;
+  g.e.res = residual;
+  g.e.y = y;
+  g.e.z = z;
+  g.e.ldr = d.ldr;
+  g.e.ldy = d.ldy;
+  g.e.ldz = d.ldz;
+  g.partial = reinterpret_cast<float*>(base + 1024);
+  g.status = reinterpret_cast<int32_t*>(base);
+  if (d.M <= moe::kLinearFewRows) {
+    MOE_CUDA_TRY(moe::launch_linear_few(g, st));
+    return MOE_OK;
+  }
+  MOE_CUDA_TRY(cudaMemsetAsync(base, 0, sizeof(int32_t), st));
+  MOE_CUDA_TRY(moe::launch_linear_gemm(g, st));
+  return MOE_OK;
+}
+
+size_t moe_linear_backward_workspace_bytes(const moe_linear_desc* desc) {
+  LinearShape d;
+  if (check_linear(desc, &d) != MOE_OK) return 0;
+  return static_cast<size_t>(plan_linear_backward(d).total);
+}
+
+moe_status moe_linear_backward(const moe_linear_desc* desc, const void* dy, const void* x,
+                               const void* w, const void* z, void* dx, void* dw, float* dbias,
+                               void* workspace, size_t ws_bytes, moe_stream_t stream) {
+  LinearShape d;
+  moe_status s = check_linear(desc, &d);
+  if (s != MOE_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!aligned(dy, desc->y_f32 ? 4 : 2) || !aligned(x, 16) || !aligned(w, 16) || !aligned(z, 2) ||
+      !aligned(dx, 16) || !aligned(dw, 16) || !aligned(dbias, 4) || !aligned(workspace, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (d.M == 0) {  // sums over no rows
+    if (dw != nullptr && d.N > 0)
+      MOE_CUDA_TRY(cudaMemsetAsync(dw, 0, static_cast<size_t>(d.N) * d.K * 2, st));
+    if (dbias != nullptr && d.N > 0)
+      MOE_CUDA_TRY(cudaMemsetAsync(dbias, 0, static_cast<size_t>(d.N) * 4, st));
+    return MOE_OK;
+  }
+  if (d.N == 0) {
+    if (dx != nullptr)
+      MOE_CUDA_TRY(cudaMemsetAsync(dx, 0, static_cast<size_t>(d.M) * d.K * 2, st));
+    return MOE_OK;
+  }
+  if (dx == nullptr && dw == nullptr && dbias == nullptr) return MOE_OK;
+  if (dy == nullptr || workspace == nullptr || (dw != nullptr && x == nullptr) ||
+      (dx != nullptr && w == nullptr) || (desc->act != MOE_ACT_NONE && z == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const LinearBackwardPlan b = plan_linear_backward(d);
+  if (ws_bytes < static_cast<size_t>(b.total)) return MOE_ERR_WORKSPACE;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  MOE_CUDA_TRY(cudaMemsetAsync(base, 0, sizeof(int32_t), st));
+  // the products take dy itself where it is already their operand
+  const bool direct = desc->act == MOE_ACT_NONE && !desc->y_f32 && d.ldy % 8 == 0 && aligned(dy, 16);
+  const bool products = dx != nullptr || dw != nullptr;
+  const void* dz = dy;
+  int64_t lddz = d.ldy;
+  if (dbias != nullptr || (products && !direct)) {
+    moe::LinearDzLaunch e;
+    e.M = d.M;
+    e.N = d.N;
+    e.act = desc->act;
+    e.dy_f32 = desc->y_f32;
+    e.dy = dy;
+    e.z = desc->act != MOE_ACT_NONE ? z : nullptr;
+    e.lddy = d.ldy;
+    e.ldz = d.ldz;
+    if (products && !direct) {
+      lddz = round_up(d.N, 8);
+      dz = base + b.dz;
+      e.dz = base + b.dz;
+      e.lddz = lddz;
+    }
+    if (dbias != nullptr) {
+      e.lines = reinterpret_cast<float*>(base + b.lines);
+      e.dbias = dbias;
+    }
+    MOE_CUDA_TRY(moe::launch_linear_dz(e, st));
+  }
+  moe::LinearLaunch g;
+  g.partial = reinterpret_cast<float*>(base + b.partial);
+  g.status = reinterpret_cast<int32_t*>(base);
+  if (dx != nullptr) {
+    g.M = d.M;
+    g.N = d.K;
+    g.K = d.N;
+    g.a_mn = 0;
+    g.b_mn = 1;
+    g.A = dz;
+    g.lda = lddz;
+    g.B = w;
+    g.ldb = d.ldw;
+    g.e.y = dx;
+    g.e.ldy = d.K;
+    MOE_CUDA_TRY(moe::launch_linear_gemm(g, st));
+  }
+  if (dw != nullptr) {
+    g.M = d.N;
+    g.N = d.K;
+    g.K = d.M;
+    g.a_mn = 1;
+    g.b_mn = 1;
+    g.A = dz;
+    g.lda = lddz;
+    g.B = x;
+    g.ldb = d.ldx;
+    g.e.y = dw;
+    g.e.ldy = d.K;
+    MOE_CUDA_TRY(moe::launch_linear_gemm(g, st));
+  }
+  return MOE_OK;
+}
+
+moe_status moe_layer_norm(int32_t M, int32_t H, int64_t ldx, int64_t ldy, int32_t x_f32,
+                          int32_t w_f32, const void* x, const void* gamma, const void* beta,
+                          float eps, void* y, float* mean, float* rstd, moe_stream_t stream) {
+  moe_status s = check_norm(M, H, &ldx, &ldy, nullptr);
+  if (s != MOE_OK) return s;
+  if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  const unsigned xa = x_f32 ? 4 : 2, wa = w_f32 ? 4 : 2;
+  if (x == nullptr || y == nullptr || !aligned(x, xa) || !aligned(y, xa) || !aligned(gamma, wa) ||
+      !aligned(beta, wa) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return MOE_ERR_INVALID_ARG;
+  moe::NormLaunch n;
+  n.M = M;
+  n.H = H;
+  n.ldx = ldx;
+  n.ldy = ldy;
+  n.x_f32 = x_f32 != 0;
+  n.w_f32 = w_f32 != 0;
+  n.x = x;
+  n.gamma = gamma;
+  n.beta = beta;
+  n.eps = eps;
+  n.y = y;
+  n.mean = mean;
+  n.rstd = rstd;
+  MOE_CUDA_TRY(moe::launch_norm(n, reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_layer_norm_backward_workspace_bytes(int32_t M, int32_t H) {
+  if (M < 0 || H < 1 || H > kMaxLinear) return 0;
+  return static_cast<size_t>(norm_backward_bytes(M, H));
+}
+
+moe_status moe_layer_norm_backward(int32_t M, int32_t H, int64_t lddy, int64_t ldx, int64_t lddx,
+                                   int32_t x_f32, int32_t w_f32, const void* dy, const void* x,
+                                   const void* gamma, const float* mean, const float* rstd, void* dx,
+                                   float* dgamma, float* dbeta, void* workspace, size_t ws_bytes,
+                                   moe_stream_t stream) {
+  moe_status s = check_norm(M, H, &ldx, &lddy, &lddx);
+  if (s != MOE_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned xa = x_f32 ? 4 : 2;
+  if (!aligned(dy, xa) || !aligned(x, xa) || !aligned(dx, xa) || !aligned(gamma, w_f32 ? 4 : 2) ||
+      !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dbeta, 4) ||
+      !aligned(workspace, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) {  // sums over no rows
+    for (float* o : {dgamma, dbeta})
+      if (o != nullptr) MOE_CUDA_TRY(cudaMemsetAsync(o, 0, static_cast<size_t>(H) * 4, st));
+    return MOE_OK;
+  }
+  const bool sums = dgamma != nullptr || dbeta != nullptr;
+  if (dx == nullptr && !sums) return MOE_OK;
+  if (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr ||
+      (sums && workspace == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (sums && ws_bytes < static_cast<size_t>(norm_backward_bytes(M, H))) return MOE_ERR_WORKSPACE;
+  moe::NormLaunch n;
+  n.M = M;
+  n.H = H;
+  n.ldx = ldx;
+  n.ldy = lddy;
+  n.lddx = lddx;
+  n.x_f32 = x_f32 != 0;
+  n.w_f32 = w_f32 != 0;
+  n.dy = dy;
+  n.x = x;
+  n.gamma = gamma;
+  n.mean = const_cast<float*>(mean);
+  n.rstd = const_cast<float*>(rstd);
+  n.dx = dx;
+  n.dgamma = dgamma;
+  n.dbeta = dbeta;
+  n.partial = sums ? static_cast<float*>(workspace) : nullptr;
+  MOE_CUDA_TRY(moe::launch_norm_backward(n, st));
   return MOE_OK;
 }
 

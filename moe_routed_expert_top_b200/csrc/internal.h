@@ -140,6 +140,96 @@ cudaError_t launch_gather_rows_any(int n_dst, int n_src, long long row_bytes, co
                                    const void* src, void* dst, int32_t* status,
                                    cudaStream_t stream);
 
+// The whole layer for a few tokens (few.cu): T <= kFewMaxTokens.
+constexpr int kFewMaxTokens = 64;
+struct FewLaunch {
+  int T = 0, H = 0, F = 0, E = 0, k = 0, F_shared = 0;
+  int score_fn = 0, renormalize = 0;
+  float scale = 1.0f;
+  const float* logits = nullptr;  // null: topk_ids / topk_weights are inputs
+  int32_t* topk_ids = nullptr;
+  float* topk_weights = nullptr;
+  const void* hidden = nullptr;
+  const void* w_gate_up = nullptr;
+  const void* w_down = nullptr;
+  const void* ws_gate_up = nullptr;
+  const void* ws_down = nullptr;
+  const void* residual = nullptr;
+  void* h = nullptr;   // bf16 [T*k, F]
+  void* hs = nullptr;  // bf16 [T, F_shared]
+  void* out = nullptr;
+  int32_t* status = nullptr;
+};
+cudaError_t launch_few(const FewLaunch& L, cudaStream_t stream);
+
+// Layer norm (norm.cu). Row pitches in elements.
+struct NormLaunch {
+  int M = 0, H = 0;
+  int x_f32 = 0;  // x, y, dy, dx fp32 rather than bf16
+  int w_f32 = 0;  // gamma, beta fp32 rather than bf16
+  float eps = 0.0f;
+  long long ldx = 0, ldy = 0, lddx = 0;  // ldy: pitch of y (forward) or dy (backward)
+  const void* x = nullptr;
+  const void* gamma = nullptr;
+  const void* beta = nullptr;
+  void* y = nullptr;
+  float* mean = nullptr;
+  float* rstd = nullptr;
+  const void* dy = nullptr;
+  void* dx = nullptr;
+  float* dgamma = nullptr;
+  float* dbeta = nullptr;
+  float* partial = nullptr;  // [2][norm_partial_rows(M, H)][H]
+};
+cudaError_t launch_norm(const NormLaunch& L, cudaStream_t stream);
+cudaError_t launch_norm_backward(const NormLaunch& L, cudaStream_t stream);
+// Upper bound of the rows of the weight gradients' partial sums.
+int norm_partial_rows(int M, int H);
+
+// The linear product (linear.cu, linear_few.cu).
+enum LinearAct { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+struct LinearEpilogue {
+  int act = kActNone;
+  int bias_f32 = 0, res_f32 = 0, y_f32 = 0;
+  const void* bias = nullptr;  // [N]
+  const void* res = nullptr;   // [M, N]
+  void* y = nullptr;           // [M, N]
+  void* z = nullptr;           // bf16 [M, N] before the activation, or null
+  long long ldr = 0, ldy = 0, ldz = 0;
+};
+// C[m, n] = epilogue(sum_k A(m, k) B(n, k)), A and B bf16. a_mn: A is stored
+// [K][M] (row k holds the M values of that k), else [M][K]; b_mn likewise.
+struct LinearLaunch {
+  int M = 0, N = 0, K = 0;
+  int a_mn = 0, b_mn = 0;
+  const void* A = nullptr;
+  const void* B = nullptr;
+  long long lda = 0, ldb = 0;  // row pitches, elements
+  LinearEpilogue e;
+  float* partial = nullptr;    // linear_gemm_partial() floats
+  int32_t* status = nullptr;
+};
+constexpr int kLinearFewRows = 64;
+cudaError_t launch_linear_few(const LinearLaunch& L, cudaStream_t stream);
+cudaError_t launch_linear_gemm(const LinearLaunch& L, cudaStream_t stream);
+long long linear_gemm_partial(int M, int N, int K, int y_f32);
+// dz bf16 [M, ldz_out] = dy * act'(z) (null: only the column sums); the sums of
+// dz's columns before rounding go to dbias through `lines` [linear_dz_lines(M)][N].
+struct LinearDzLaunch {
+  int M = 0, N = 0, act = kActNone, dy_f32 = 0;
+  const void* dy = nullptr;
+  const void* z = nullptr;
+  long long lddy = 0, ldz = 0, lddz = 0;
+  void* dz = nullptr;
+  float* lines = nullptr;
+  float* dbias = nullptr;
+};
+cudaError_t launch_linear_dz(const LinearDzLaunch& L, cudaStream_t stream);
+int linear_dz_lines(int M);
+// out[i][c] = sum over lines l (in order) of table[i][l][c], i < tables.
+cudaError_t launch_sum_lines(const float* table, int tables, int lines, int H, float* out0,
+                             float* out1, cudaStream_t stream);
+
 // Streaming multiprocessors of the current device (cached per device).
 int device_sm_count();
 

@@ -1,7 +1,9 @@
 """Layer objects around the C entry points: ``RoutedExperts``
 (``moe_experts_forward``), ``SharedExpert`` (``moe_shared_expert_forward``,
 one tensor-parallel rank) and ``SharedFusedMoE`` (both, with the partial
-output contract).
+output contract); ``FewTokenExperts`` (``moe_experts_forward_few``, a decode
+step's whole layer), ``Linear`` and ``LayerNorm`` with their backward passes, and
+``FeedForwardBlock``, which runs norm, router and experts.
 
 Each owns its weights (device tensors) and a workspace buffer sized by the
 library; ``forward`` only marshals pointers into the C entry points. FP8 down
@@ -10,11 +12,16 @@ weights are prepared once with ``moe_quantize_weight_128x128`` when
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
-from . import (make_problem, moe_experts_forward, moe_quantize_weight_128x128,
-               moe_route_topk, moe_shared_expert_forward, moe_shared_workspace_bytes,
-               moe_workspace_bytes)
+from . import (MOE_FEW_MAX_TOKENS, make_linear_desc, make_problem, moe_experts_forward,
+               moe_experts_forward_few, moe_few_workspace_bytes, moe_layer_norm,
+               moe_layer_norm_backward, moe_layer_norm_backward_workspace_bytes, moe_linear,
+               moe_linear_backward, moe_linear_backward_workspace_bytes,
+               moe_linear_workspace_bytes, moe_quantize_weight_128x128, moe_route_topk,
+               moe_shared_expert_forward, moe_shared_workspace_bytes, moe_workspace_bytes)
 
 
 class RoutedExperts:
@@ -159,3 +166,299 @@ class SharedFusedMoE:
             import torch.distributed as dist
             dist.all_reduce(shared_partial, op=dist.ReduceOp.SUM, group=group)
         return (shared_partial.float() + routed_out.float()).to(torch.bfloat16)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on_device_of(t: torch.Tensor):
+    """Context in which the tensor's device is the current one: the library
+    launches on the current device and its current stream."""
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if t.device.index == torch.cuda.current_device():
+        return _SAME_DEVICE
+    return torch.cuda.device(t.device)
+
+
+def _matrix(t: torch.Tensor, name: str, shape, dtypes, device) -> int:
+    """Checks a matrix whose rows are dense; returns its row pitch (0 where one
+    row or less leaves it open)."""
+    if not torch.is_tensor(t) or t.dim() != 2 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} needs rows of stride 1")
+    if t.shape[0] <= 1 or t.shape[1] == 0:
+        return 0
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows overlap")
+    return t.stride(0)
+
+
+def _vector(t: torch.Tensor | None, name: str, n: int, device):
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be a bfloat16 or float32 vector of {n}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.contiguous()
+
+
+class FewTokenExperts:
+    """The whole routed layer for 1..64 tokens, routing included, in two kernels
+    (``moe_experts_forward_few``): a decode step. Arguments and weight layouts as
+    ``RoutedExperts``, bf16 weights only. Every ``forward`` takes its own
+    workspace from torch's allocator, so calls on several streams and in several
+    captured graphs do not share one."""
+
+    def __init__(self, w_gate_up: torch.Tensor, w_down: torch.Tensor, top_k: int,
+                 score_fn: str = "softmax", renormalize: bool = True,
+                 routed_scaling_factor: float = 1.0, ws_gate_up: torch.Tensor | None = None,
+                 ws_down: torch.Tensor | None = None):
+        E, two_f, H = w_gate_up.shape
+        self.E, self.F, self.H = E, two_f // 2, H
+        if two_f % 2 or tuple(w_down.shape) != (E, H, self.F):
+            raise ValueError("need w_gate_up [E, 2F, H] and w_down [E, H, F]")
+        if (ws_gate_up is None) != (ws_down is None):
+            raise ValueError("the shared expert needs both ws_gate_up and ws_down")
+        self.F_shared = 0 if ws_gate_up is None else ws_gate_up.shape[0] // 2
+        if ws_gate_up is not None and (tuple(ws_gate_up.shape) != (2 * self.F_shared, H) or
+                                       tuple(ws_down.shape) != (H, self.F_shared)):
+            raise ValueError("need ws_gate_up [2*F_s, H] and ws_down [H, F_s]")
+        for t in (w_gate_up, w_down, ws_gate_up, ws_down):
+            if t is not None and (t.dtype != torch.bfloat16 or t.device != w_gate_up.device):
+                raise ValueError("weights must be bfloat16 tensors on one device")
+        self.top_k, self.score_fn, self.renormalize = top_k, score_fn, renormalize
+        self.scale = float(routed_scaling_factor)
+        self.w_gate_up, self.w_down = w_gate_up.contiguous(), w_down.contiguous()
+        self.ws_gate_up = None if ws_gate_up is None else ws_gate_up.contiguous()
+        self.ws_down = None if ws_down is None else ws_down.contiguous()
+        self.device = w_gate_up.device
+        self._problems = {}  # T -> (problem, workspace bytes)
+        self._ws = None
+
+    def problem(self, T: int):
+        return make_problem(T=T, H=self.H, F=self.F, E=self.E, top_k=self.top_k,
+                            score_fn=self.score_fn, renormalize=self.renormalize,
+                            routed_scaling_factor=self.scale, F_shared=self.F_shared)
+
+    def forward(self, hidden: torch.Tensor, topk_ids: torch.Tensor | None = None,
+                topk_weights: torch.Tensor | None = None, logits: torch.Tensor | None = None,
+                residual: torch.Tensor | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+        """``out`` [T, H] from ``hidden`` and either ``logits`` fp32 [T, E] (then
+        ``topk_ids`` / ``topk_weights``, where given, receive the routing) or
+        given ``topk_ids`` int32 and ``topk_weights`` fp32 [T, k]."""
+        T = hidden.shape[0]
+        if T > MOE_FEW_MAX_TOKENS:
+            raise ValueError(f"at most {MOE_FEW_MAX_TOKENS} tokens, not {T}: use RoutedExperts")
+        for t, name, cols, dtype in ((hidden, "hidden", self.H, torch.bfloat16),
+                                     (logits, "logits", self.E, torch.float32),
+                                     (topk_ids, "topk_ids", self.top_k, torch.int32),
+                                     (topk_weights, "topk_weights", self.top_k, torch.float32),
+                                     (residual, "residual", self.H, torch.bfloat16),
+                                     (out, "out", self.H, torch.bfloat16)):
+            if t is None:
+                continue
+            if t.dtype != dtype or t.shape != (T, cols) or t.device != self.device:
+                raise ValueError(f"{name} must be {dtype} [{T}, {cols}] on {self.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if logits is None and (topk_ids is None or topk_weights is None):
+            raise ValueError("need logits, or topk_ids and topk_weights")
+        known = self._problems.get(T)
+        if known is None:
+            prob = self.problem(T)
+            known = self._problems[T] = (prob, moe_few_workspace_bytes(prob))
+        with _on_device_of(hidden):
+            if out is None:
+                out = torch.empty_like(hidden)
+            self._ws = ws = torch.empty(max(known[1], 1024), dtype=torch.uint8, device=self.device)
+            moe_experts_forward_few(known[0], hidden, logits, topk_ids, topk_weights,
+                                    self.w_gate_up, self.w_down, self.ws_gate_up, self.ws_down,
+                                    self.scale, residual, out, ws, ws.shape[0])
+        return out
+
+    def device_status(self) -> int:
+        """The device status word of the last forward (synchronises)."""
+        return int(self._ws[:4].view(torch.int32).item())
+
+
+class Linear:
+    """``y = act(x W^T + bias) + residual`` (``moe_linear``) and its backward pass.
+    ``weight`` bf16 [N, K], ``bias`` bf16 or fp32 [N] or None, ``activation`` one of
+    none, relu, silu, gelu, ``out_dtype`` bf16, or fp32 (router logits)."""
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None,
+                 activation: str = "none", out_dtype: torch.dtype = torch.bfloat16):
+        if weight.dim() != 2:
+            raise ValueError("weight must be [N, K]")
+        self.N, self.K = weight.shape
+        if activation not in ("none", "relu", "silu", "gelu"):
+            raise ValueError(f"unknown activation {activation!r}")
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype must be bfloat16 or float32")
+        self.device = weight.device
+        self.ldw = _matrix(weight, "weight", weight.shape, (torch.bfloat16,), self.device)
+        self.weight = weight
+        self.bias = _vector(bias, "bias", self.N, self.device)
+        self.activation, self.out_dtype = activation, out_dtype
+        self._ws = None
+
+    def _desc(self, M, ldx=0, ldr=0, ldy=0, ldz=0, res_f32=False):
+        return make_linear_desc(M, self.N, self.K, self.activation,
+                                self.bias is not None and self.bias.dtype == torch.float32, res_f32,
+                                self.out_dtype == torch.float32, ldx, self.ldw, ldr, ldy, ldz)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, with_z: bool = False):
+        """y [M, N], or (y, z) ``with_z``: z bf16 is what ``backward`` needs beside
+        x unless the activation is none."""
+        M = x.shape[0]
+        dev = self.device
+        ldx = _matrix(x, "x", (M, self.K), (torch.bfloat16,), dev)
+        ldr = 0 if residual is None else _matrix(residual, "residual", (M, self.N),
+                                                 (torch.bfloat16, torch.float32), dev)
+        ldy = 0 if out is None else _matrix(out, "out", (M, self.N), (self.out_dtype,), dev)
+        with _on_device_of(x):
+            if out is None:
+                out = torch.empty(M, self.N, dtype=self.out_dtype, device=dev)
+            z = torch.empty(M, self.N, dtype=torch.bfloat16, device=dev) if with_z else None
+            d = self._desc(M, ldx, ldr, ldy, 0, residual is not None and
+                           residual.dtype == torch.float32)
+            need = moe_linear_workspace_bytes(d)
+            self._ws = ws = torch.empty(max(need, 1024), dtype=torch.uint8, device=dev)
+            moe_linear(d, x, self.weight, self.bias, residual, out, z, ws, ws.shape[0])
+        return (out, z) if with_z else out
+
+    def backward(self, dy: torch.Tensor, x: torch.Tensor, z: torch.Tensor | None = None,
+                 need_dx: bool = True, need_dw: bool = True, need_dbias: bool | None = None):
+        """(dx, dw, dbias) from dy [M, N] of ``out_dtype``, the forward's x and,
+        unless the activation is none, its z; what is not needed comes as None.
+        dbias is fp32; the residual's gradient is dy."""
+        M = dy.shape[0]
+        dev = self.device
+        if need_dbias is None:
+            need_dbias = self.bias is not None
+        if self.activation != "none" and z is None:
+            raise ValueError("backward of an activation needs the forward's z")
+        if self.activation == "none":
+            z = None
+        ldy = _matrix(dy, "dy", (M, self.N), (self.out_dtype,), dev)
+        ldx = _matrix(x, "x", (M, self.K), (torch.bfloat16,), dev)
+        ldz = 0 if z is None else _matrix(z, "z", (M, self.N), (torch.bfloat16,), dev)
+        with _on_device_of(x):
+            dx = torch.empty(M, self.K, dtype=torch.bfloat16, device=dev) if need_dx else None
+            dw = torch.empty(self.N, self.K, dtype=torch.bfloat16, device=dev) if need_dw else None
+            db = torch.empty(self.N, dtype=torch.float32, device=dev) if need_dbias else None
+            d = self._desc(M, ldx, 0, ldy, ldz)
+            need = moe_linear_backward_workspace_bytes(d)
+            self._ws = ws = torch.empty(max(need, 1024), dtype=torch.uint8, device=dev)
+            moe_linear_backward(d, dy, x, self.weight, z, dx, dw, db, ws, ws.shape[0])
+        return dx, dw, db
+
+    def device_status(self) -> int:
+        """The device status word of the last call (synchronises)."""
+        return int(self._ws[:4].view(torch.int32).item())
+
+
+class LayerNorm:
+    """Layer norm over the last dimension of [M, H] (``moe_layer_norm``) and its
+    backward pass; x bf16 or fp32, ``weight`` and ``bias`` [H] of one dtype or None."""
+
+    def __init__(self, weight: torch.Tensor | None, bias: torch.Tensor | None = None,
+                 eps: float = 1e-5):
+        self.weight = None if weight is None else _vector(weight, "weight", weight.shape[0],
+                                                          weight.device)
+        self.bias = None if bias is None else _vector(bias, "bias", bias.shape[0], bias.device)
+        if weight is not None and bias is not None and (
+                weight.dtype != bias.dtype or weight.shape != bias.shape or
+                weight.device != bias.device):
+            raise ValueError("weight and bias must have the same dtype, size and device")
+        if not eps >= 0.0:
+            raise ValueError("eps must not be negative")
+        self.eps = float(eps)
+        w = weight if weight is not None else bias
+        self.H = None if w is None else w.shape[0]
+        self.device = None if w is None else w.device
+        self.w_f32 = w is not None and w.dtype == torch.float32
+
+    def _check(self, x: torch.Tensor):
+        if x.dim() != 2 or x.shape[1] < 1 or (self.H is not None and x.shape[1] != self.H):
+            raise ValueError(f"x must be [M, {'H' if self.H is None else self.H}]")
+        return _matrix(x, "x", x.shape, (torch.bfloat16, torch.float32), self.device or x.device)
+
+    def forward(self, x: torch.Tensor, out: torch.Tensor | None = None, stats: bool = False):
+        """y, or (y, mean, rstd) with ``stats``: what ``backward`` needs beside x."""
+        ldx = self._check(x)
+        M, H = x.shape
+        ldy = 0 if out is None else _matrix(out, "out", x.shape, (x.dtype,), x.device)
+        with _on_device_of(x):
+            if out is None:
+                out = torch.empty(M, H, dtype=x.dtype, device=x.device)
+            mean = rstd = None
+            if stats:
+                mean = torch.empty(M, dtype=torch.float32, device=x.device)
+                rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+            moe_layer_norm(M, H, ldx, ldy, x.dtype == torch.float32, self.w_f32, x, self.weight,
+                           self.bias, self.eps, out, mean, rstd)
+        return (out, mean, rstd) if stats else out
+
+    def backward(self, dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                 need_dx: bool = True, need_weights: bool = True):
+        """(dx, dweight, dbias): dx of x's dtype, the weight gradients fp32; what is
+        not needed comes as None."""
+        ldx = self._check(x)
+        M, H = x.shape
+        lddy = _matrix(dy, "dy", x.shape, (x.dtype,), x.device)
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            if t.shape != (M,) or t.dtype != torch.float32 or t.device != x.device or \
+                    not t.is_contiguous():
+                raise ValueError(f"{name} must be a dense float32 vector of {M}")
+        with _on_device_of(x):
+            dx = torch.empty(M, H, dtype=x.dtype, device=x.device) if need_dx else None
+            dw = db = ws = None
+            if need_weights:
+                dw = torch.empty(H, dtype=torch.float32, device=x.device)
+                db = torch.empty(H, dtype=torch.float32, device=x.device)
+                ws = torch.empty(moe_layer_norm_backward_workspace_bytes(M, H), dtype=torch.uint8,
+                                 device=x.device)
+            moe_layer_norm_backward(M, H, lddy, ldx, 0, x.dtype == torch.float32, self.w_f32, dy, x,
+                                    self.weight, mean, rstd, dx, dw, db, ws)
+        return dx, dw, db
+
+
+class FeedForwardBlock:
+    """``x + experts(norm(x))``: layer norm, the router's product (fp32 logits), the
+    routed experts with their shared expert, and the residual. Up to 64 tokens
+    (a decode step) run as ``FewTokenExperts``, with the residual added before
+    the one rounding of the output; more as ``RoutedExperts``, whose bf16 output
+    the residual is added to (one rounding more). ``routed`` must hold bf16
+    weights for the few-token form; with FP8 down weights every size goes to
+    ``RoutedExperts``."""
+
+    def __init__(self, norm: LayerNorm, router: Linear, routed: RoutedExperts):
+        if router.N != routed.E or router.K != routed.H or router.out_dtype != torch.float32:
+            raise ValueError("the router must give fp32 logits [T, E] from [T, H]")
+        if norm.H is not None and norm.H != routed.H:
+            raise ValueError("the norm's size must be the experts' H")
+        self.norm, self.router, self.routed = norm, router, routed
+        self.few = None
+        if not routed.down_fp8:
+            self.few = FewTokenExperts(routed.w_gate_up, routed.w_down, routed.top_k,
+                                       routed.score_fn, routed.renormalize, routed.scale,
+                                       routed.ws_gate_up, routed.ws_down)
+
+    def forward(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        hidden = self.norm.forward(x)
+        logits = self.router.forward(hidden)
+        if self.few is not None and x.shape[0] <= MOE_FEW_MAX_TOKENS:
+            return self.few.forward(hidden, logits=logits, residual=x, out=out)
+        ids, weights = self.routed.route(logits)
+        routed = self.routed.forward(hidden, ids, weights)
+        return torch.add(x, routed, out=out)
