@@ -176,12 +176,13 @@ moe_status check_few(const moe_problem* pr) {
 }
 
 struct FewPlan {
-  int64_t h = 0, hs = 0, total = 0;
+  int64_t list = 0, h = 0, hs = 0, total = 0;
 };
 
 FewPlan plan_few(const moe_problem* pr) {
   FewPlan w;
-  w.h = 1024;  // after the status word
+  w.list = 1024;  // after the status word
+  w.h = round_up(w.list + static_cast<int64_t>(moe::few_list_bytes_of(pr->E, pr->T * pr->top_k)), 1024);
   w.hs = round_up(w.h + static_cast<int64_t>(pr->T) * pr->top_k * pr->F * 2, 1024);
   w.total = round_up(w.hs + static_cast<int64_t>(pr->T) * pr->F_shared * 2, 1024);
   return w;
@@ -956,6 +957,7 @@ moe_status moe_experts_forward_few(const moe_problem* prob, const void* hidden, 
   f.ws_gate_up = ws_gate_up;
   f.ws_down = ws_down;
   f.residual = residual;
+  f.list = base + w.list;
   f.h = base + w.h;
   f.hs = base + w.hs;
   f.out = out;

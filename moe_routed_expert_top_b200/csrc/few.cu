@@ -8,13 +8,13 @@
 // What bounds it: with so few tokens every touched expert's 3*H*F weights are
 // read once from HBM and meet 1..64 rows each, so the time is the weights'
 // bytes over the memory rate plus the fixed cost of the launches. The kernels
-// therefore (a) give every CTA the same number of weight ROWS, to within one
-// row, whatever the routing; (b) read each row exactly once, straight into the
-// registers of the warp that multiplies it (32 bytes a lane, the next chunk in
-// flight while this one is multiplied); (c) rebuild the routing in every CTA
-// from the logits, which costs less than a third launch and lets the second
-// kernel start its weight loads before the first has ended (programmatic
-// dependent launch).
+// therefore (a) give every CTA about the same number of weight rows whatever the
+// routing; (b) read each row exactly once, straight into the registers of the
+// warp that multiplies it (32 bytes a lane, the next steps in flight while one
+// is multiplied); (c) route in the first kernel, every CTA for itself from the
+// logits, which costs less than a launch; one CTA leaves the list of experts and
+// tokens for the second kernel, whose launch overlaps the first's end
+// (programmatic dependent launch).
 //
 // The products themselves (mma.sync from registers) are in few.cuh.
 #include <cuda_bf16.h>
@@ -31,6 +31,12 @@
 namespace moe {
 
 namespace {
+
+// Steps of 4 KB that each of the 8 warps has in flight: 128 KB an SM. Measured
+// against 12 warps x 3 and 16 x 2 (as many bytes, fewer registers a thread): 13
+// tokens of 128 small experts 127 us, 157 and 169; 64 tokens of 256 large ones
+// 3.17 ms, 3.39 and 3.55; up to 8 tokens the three are within 2%.
+constexpr int kDepth = 4;
 
 struct FewParams {
   int T, H, F, E, k, Fs;
@@ -49,46 +55,57 @@ struct FewParams {
   __nv_bfloat16* hs;
   __nv_bfloat16* out;
   int32_t* status;
+  uint4* list;        // the routing, from kernel 1 to kernel 2
 };
 
-// The routing of all tokens, in shared memory.
+// The routing of all tokens: what both kernels use (the list), then what builds it.
+// An expert's tokens come in groups of at most kFewGroup; an expert with more
+// (of at most 64) has several groups, and its weights are read once for each
+// (from L2 after the first: the groups' tiles run at about the same time).
+constexpr int kFewGroup = 16;
 struct FewRoute {
-  unsigned long long* mask;  // [E] tokens of each expert, as bits
+  int* n_act;                // groups
+  int* act_e;                // [A] their experts, in index order; A = few_groups(E, P)
+  int* act_off;              // [A + 1] first pair of each of them
   float* weight;             // [P] weight of a pair, in expert order
-  int* act_e;                // [E] experts with tokens, in index order
-  int* act_off;              // [E + 1] first pair of each of them
-  short* ids;                // [P] expert of pair (t, j), -1 = none
-  float* raw;                // [P] weight of pair (t, j)
   uint8_t* tok;              // [P] token of a pair, in expert order
-  int* n_act;
+  unsigned long long* mask;  // [E] tokens of each expert, as bits
+  float* raw;                // [P] weight of pair (t, j)
+  short* ids;                // [P] expert of pair (t, j), -1 = none
   int* bad;
 };
 
 __host__ __device__ inline size_t few_up16(size_t v) { return (v + 15) & ~static_cast<size_t>(15); }
 
+__host__ __device__ inline int few_groups(int E, int P) { return (E < P ? E : P) + P / kFewGroup; }
+__host__ __device__ inline size_t few_list_bytes(int E, int P) {
+  const int A = few_groups(E, P);
+  return 16 + few_up16(4ull * A) + few_up16(4ull * (A + 1)) + few_up16(4ull * P) + few_up16(P);
+}
 __host__ __device__ inline size_t few_route_bytes(int E, int P) {
-  return few_up16(8ull * E) + few_up16(4ull * P) + few_up16(4ull * E) + few_up16(4ull * (E + 1)) +
-         few_up16(2ull * P) + few_up16(4ull * P) + few_up16(P) + 64;
+  return few_list_bytes(E, P) + few_up16(8ull * E) + few_up16(4ull * P) + few_up16(2ull * P) + 16;
 }
 
 __device__ __forceinline__ FewRoute few_route_layout(uint8_t* s, int E, int P) {
+  const int A = few_groups(E, P);
   FewRoute r;
-  r.mask = reinterpret_cast<unsigned long long*>(s);
-  s += few_up16(8ull * E);
-  r.weight = reinterpret_cast<float*>(s);
-  s += few_up16(4ull * P);
+  r.n_act = reinterpret_cast<int*>(s);
+  s += 16;
   r.act_e = reinterpret_cast<int*>(s);
-  s += few_up16(4ull * E);
+  s += few_up16(4ull * A);
   r.act_off = reinterpret_cast<int*>(s);
-  s += few_up16(4ull * (E + 1));
-  r.ids = reinterpret_cast<short*>(s);
-  s += few_up16(2ull * P);
-  r.raw = reinterpret_cast<float*>(s);
+  s += few_up16(4ull * (A + 1));
+  r.weight = reinterpret_cast<float*>(s);
   s += few_up16(4ull * P);
   r.tok = s;
   s += few_up16(P);
-  r.n_act = reinterpret_cast<int*>(s);
-  r.bad = r.n_act + 1;
+  r.mask = reinterpret_cast<unsigned long long*>(s);
+  s += few_up16(8ull * E);
+  r.raw = reinterpret_cast<float*>(s);
+  s += few_up16(4ull * P);
+  r.ids = reinterpret_cast<short*>(s);
+  s += few_up16(2ull * P);
+  r.bad = reinterpret_cast<int*>(s);
   return r;
 }
 
@@ -104,37 +121,35 @@ __device__ __forceinline__ float few_unkey(uint32_t key) {
 
 // Top-k of one token by one warp, with the weights of route_topk_kernel bit for
 // bit (largest logit first, then the lowest index; sums in slot order). Lane
-// l holds experts l, l + 32, ...; the result of slot j is lane j's.
+// l holds experts l, l + 32, ... (kPer of them); the result of slot j is lane j's.
+template <int kPer>
 __device__ __forceinline__ void few_topk(const float* row, int E, int k, int score_fn,
                                          int renormalize, int& my_id, float& my_w) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[32];
+  uint32_t key[kPer];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    key[i] = 0;
-    if (32 * i < E && lane + 32 * i < E) key[i] = few_key(__ldg(row + lane + 32 * i));
+  for (int i = 0; i < kPer; ++i) {
+    const float v = lane + 32 * i < E ? __ldg(row + lane + 32 * i) : 0.0f;
+    key[i] = lane + 32 * i < E ? few_key(v) : 0u;
   }
   uint32_t my_key = 0x80000000u;
   my_id = -1;
   for (int j = 0; j < k; ++j) {
     uint32_t best = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (32 * i < E) best = max(best, key[i]);
+    for (int i = 0; i < kPer; ++i) best = max(best, key[i]);
     best = __reduce_max_sync(0xffffffffu, best);
-    int at = INT_MAX;
+    unsigned at = 0xffffffffu;
 #pragma unroll
-    for (int i = 31; i >= 0; --i)
-      if (32 * i < E && key[i] == best) at = lane + 32 * i;
+    for (int i = kPer - 1; i >= 0; --i)
+      if (key[i] == best) at = lane + 32 * i;
     at = __reduce_min_sync(0xffffffffu, at);
-    if ((at & 31) == lane) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if ((at >> 5) == i) key[i] = 0;
-    }
+    for (int i = 0; i < kPer; ++i)
+      if (at == static_cast<unsigned>(lane + 32 * i)) key[i] = 0;
     if (lane == j) {
       my_key = best;
-      my_id = at;
+      my_id = static_cast<int>(at);
     }
   }
   const float val = few_unkey(my_key);
@@ -170,7 +185,7 @@ __device__ __forceinline__ void few_topk(const float* row, int E, int k, int sco
 // and its tokens fit one 64-bit mask: a pair's place in expert order is then a
 // bit count, with no atomics deciding an order. `publish`: this CTA also writes
 // the ids, the weights and the status word to global memory.
-__device__ void few_route(const FewParams& p, const FewRoute& r, bool publish, int* scratch) {
+__device__ __forceinline__ void few_route(const FewParams& p, const FewRoute& r, bool publish, int* scratch) {
   const int P = p.T * p.k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < p.E; e += kFewThreads) r.mask[e] = 0ull;
@@ -179,7 +194,11 @@ __device__ void few_route(const FewParams& p, const FewRoute& r, bool publish, i
     for (int t = warp; t < p.T; t += kFewWarps) {
       int id;
       float w;
-      few_topk(p.logits + static_cast<int64_t>(t) * p.E, p.E, p.k, p.score_fn, p.renormalize, id, w);
+      const float* row = p.logits + static_cast<int64_t>(t) * p.E;
+      if (p.E <= 256)
+        few_topk<8>(row, p.E, p.k, p.score_fn, p.renormalize, id, w);
+      else
+        few_topk<32>(row, p.E, p.k, p.score_fn, p.renormalize, id, w);
       if (lane < p.k) {
         r.ids[t * p.k + lane] = static_cast<short>(id);
         r.raw[t * p.k + lane] = w;
@@ -204,13 +223,13 @@ __device__ void few_route(const FewParams& p, const FewRoute& r, bool publish, i
     if (id >= 0) atomicOr(&r.mask[id], 1ull << (i / p.k));
   }
   __syncthreads();
-  // exclusive scan over the experts of (pairs, experts with pairs)
+  // exclusive scan over the experts of (pairs, groups)
   const int per = (p.E + kFewThreads - 1) / kFewThreads;
   const int beg = threadIdx.x * per;
   uint32_t local = 0;
   for (int i = 0; i < per && beg + i < p.E; ++i) {
     const int n = __popcll(r.mask[beg + i]);
-    local += (static_cast<uint32_t>(n) << 12) + (n > 0 ? 1u : 0u);
+    local += (static_cast<uint32_t>(n) << 12) + (n + kFewGroup - 1) / kFewGroup;
   }
   uint32_t inc = local;
 #pragma unroll
@@ -227,8 +246,10 @@ __device__ void few_route(const FewParams& p, const FewRoute& r, bool publish, i
     const int n = __popcll(m);
     if (n > 0) {
       const int a = static_cast<int>(run & 0xFFFu), off = static_cast<int>(run >> 12);
-      r.act_e[a] = beg + i;
-      r.act_off[a] = off;
+      for (int c = 0; c * kFewGroup < n; ++c) {
+        r.act_e[a + c] = beg + i;
+        r.act_off[a + c] = off + c * kFewGroup;
+      }
       // the pairs of this expert, in token order
       unsigned long long left = m;
       for (int c = 0; c < n; ++c) {
@@ -241,7 +262,7 @@ __device__ void few_route(const FewParams& p, const FewRoute& r, bool publish, i
         r.weight[off + c] = w;
       }
     }
-    run += (static_cast<uint32_t>(n) << 12) + (n > 0 ? 1u : 0u);
+    run += (static_cast<uint32_t>(n) << 12) + (n + kFewGroup - 1) / kFewGroup;
   }
   if (threadIdx.x == kFewThreads - 1) {
     *r.n_act = static_cast<int>(run & 0xFFFu);
@@ -249,148 +270,236 @@ __device__ void few_route(const FewParams& p, const FewRoute& r, bool publish, i
   }
   if (publish && threadIdx.x == 0) *p.status = *r.bad ? MOE_DEV_BAD_EXPERT_ID_FLAG : 0;
   __syncthreads();
+  if (publish) {
+    // the list for kernel 2, in the layout that it has in shared memory
+    const uint4* src = reinterpret_cast<const uint4*>(r.n_act);
+    for (int i = threadIdx.x; i < static_cast<int>(few_list_bytes(p.E, P) / 16); i += kFewThreads)
+      p.list[i] = src[i];
+  }
+}
+
+// Kernel 2's: the list as kernel 1 left it.
+__device__ __forceinline__ void few_route_load(const FewParams& p, const FewRoute& r) {
+  uint4* dst = reinterpret_cast<uint4*>(r.n_act);
+  for (int i = threadIdx.x; i < static_cast<int>(few_list_bytes(p.E, p.T * p.k) / 16); i += kFewThreads)
+    dst[i] = p.list[i];
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
 // Kernel 1: h = bf16(silu(Wg x) * (Wu x)) for every pair.
-// The rows of all active experts (and of the shared expert) form one list of
-// gate/up row pairs; CTA c takes an equal share of it, in tiles of up to 16
-// pairs of one expert. In a tile the warps split k in chunks of 64 and add
-// their sums through shared memory.
+// The gate/up row pairs of the active experts (and of the shared expert) are cut
+// into tiles of up to 16 pairs of one expert, and CTA c takes tiles c, c + grid,
+// ...: experts with many tokens, whose tiles cost more, spread over all CTAs. In a tile the warps split k in chunks of 64 and add
+// their sums through shared memory. A warp's loads run kDepth steps ahead, over
+// the ends of tiles, so the sums' barrier does not empty the memory pipe.
 // ---------------------------------------------------------------------------
 struct UpTile {
   const __nv_bfloat16* gate;  // first gate row (row pitch H); null: no tile
   int64_t up;                 // elements from a gate row to its up row
+  const __nv_bfloat16* x0;    // the lane's row of the first 8 tokens; null: none
   int rows;                   // 1..16
-  int off, n;                 // the expert's pairs (shared: off -1, n = T)
+  int t0;                     // the shared expert's first token of the group; -1: a routed one
+  int off, n;                 // the group's first pair, its tokens
   int f0;
+  uint64_t policy;
 };
 
-__device__ __forceinline__ UpTile up_tile(const FewParams& p, const FewRoute& r, int n_act, int64_t u,
-                                          int64_t u1) {
+struct UpPlan {
+  int per_e, per_s;  // tiles of a group, of a group of the shared expert
+  uint64_t once, again;  // L2 policies of weights that one group reads, that several do
+  int tiles;
+};
+
+// As many tiles a CTA as rows of at most 16 pairs need, and then rows that make
+// these tiles equal: 8 experts of 768 over 148 CTAs are 3 tiles of 14 a CTA.
+__device__ __forceinline__ UpPlan up_plan(const FewParams& p, int n_act) {
+  const int groups_s = p.Fs > 0 ? (p.T + kFewGroup - 1) / kFewGroup : 0;
+  const int units = n_act * p.F + groups_s * p.Fs, grid = gridDim.x;
+  const int turns = max(1, (units + 16 * grid - 1) / (16 * grid));
+  const int rows = min(16, max(1, (units + grid * turns - 1) / (grid * turns)));
+  UpPlan u;
+  u.per_e = (p.F + rows - 1) / rows;
+  u.per_s = (p.Fs + rows - 1) / rows;
+  u.tiles = n_act * u.per_e + groups_s * u.per_s;
+  u.once = l2_policy_evict_first();
+  u.again = l2_policy_evict_normal();
+  return u;
+}
+
+__device__ __forceinline__ UpTile up_tile(const FewParams& p, const FewRoute& r, const UpPlan& u,
+                                          int n_act, int i) {
   UpTile t;
   t.gate = nullptr;
+  t.x0 = nullptr;
   t.rows = 0;
   t.n = 0;
   t.off = 0;
   t.f0 = 0;
   t.up = 0;
-  if (u >= u1) return t;
-  const int64_t routed = static_cast<int64_t>(n_act) * p.F;
-  int F;
+  t.t0 = -1;
+  t.policy = u.once;
+  if (i >= u.tiles) return t;
+  const int g = (threadIdx.x & 31) >> 2;
+  int F = p.F, per = u.per_e, c;
   const __nv_bfloat16* w;
-  if (u < routed) {
-    const int a = static_cast<int>(u / p.F);
-    t.f0 = static_cast<int>(u - static_cast<int64_t>(a) * p.F);
-    F = p.F;
+  if (i < n_act * u.per_e) {
+    const int a = i / u.per_e, e = r.act_e[a];
+    c = i - a * u.per_e;
     t.off = r.act_off[a];
     t.n = r.act_off[a + 1] - t.off;
-    w = p.w_gate_up + static_cast<int64_t>(r.act_e[a]) * 2 * p.F * p.H;
+    if (t.n == kFewGroup || (a > 0 && r.act_e[a - 1] == e)) t.policy = u.again;
+    w = p.w_gate_up + static_cast<int64_t>(e) * 2 * p.F * p.H;
+    if (g < t.n) t.x0 = p.x + static_cast<int64_t>(r.tok[t.off + g]) * p.H;
   } else {
-    t.f0 = static_cast<int>(u - routed);
     F = p.Fs;
-    t.off = -1;
-    t.n = p.T;
+    per = u.per_s;
+    const int a = (i - n_act * u.per_e) / per;
+    c = i - n_act * u.per_e - a * per;
+    t.t0 = a * kFewGroup;
+    t.n = min(kFewGroup, p.T - t.t0);
+    if (p.T > kFewGroup) t.policy = u.again;
     w = p.ws_gate_up;
+    if (g < t.n) t.x0 = p.x + static_cast<int64_t>(t.t0 + g) * p.H;
   }
-  const int64_t room = min(static_cast<int64_t>(F - t.f0), u1 - u);
-  t.rows = room < 16 ? static_cast<int>(room) : 16;
+  t.f0 = static_cast<int>(static_cast<int64_t>(F) * c / per);
+  t.rows = static_cast<int>(static_cast<int64_t>(F) * (c + 1) / per) - t.f0;
   t.gate = w + static_cast<int64_t>(t.f0) * p.H;
   t.up = static_cast<int64_t>(F) * p.H;
   return t;
 }
 
+// A warp's loads of one step: weights of 64 k, and the first 8 tokens' words.
+struct FewStep {
+  FewA a;
+  uint4 b[2];
+};
+
+// acc += A B for a step: the first token tile's words are there, the others' are
+// loaded (x: from L1 after the expert's first tile).
 template <int NT>
-__global__ void __launch_bounds__(kFewThreads, 2) few_up_kernel(const FewParams p) {
+__device__ __forceinline__ void few_step(float (&acc)[NT][2][4], const FewStep& st, int nt,
+                                         const __nv_bfloat16* const (&xr)[NT], int kofs, bool on) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    if (j < nt) {
+      uint4 b[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        b[s] = j == 0 ? st.b[s] : few_ldx(xr[j] + kofs + 8 * s, on && xr[j] != nullptr);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint32_t* lo = st.a.v[m][0].r + 4 * s;
+          const uint32_t* hi = st.a.v[m][1].r + 4 * s;
+          few_mma(acc[j][m], lo[0], hi[0], lo[1], hi[1], b[s].x, b[s].y);
+          few_mma(acc[j][m], lo[2], hi[2], lo[3], hi[3], b[s].z, b[s].w);
+        }
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads, 1) few_up_kernel(const FewParams p) {
   extern __shared__ __align__(16) uint8_t few_smem[];
   __shared__ int scratch[kFewWarps];
   const int P = p.T * p.k;
   const FewRoute r = few_route_layout(few_smem, p.E, P);
-  // [warp][token tile][gate/up][lane] sums of the warps
-  float4* red = reinterpret_cast<float4*>(few_smem + few_route_bytes(p.E, P));
+  // [flip][warp][gate/up][lane][4] sums of the warps, one token tile at a time
+  float* red = reinterpret_cast<float*>(few_smem + few_route_bytes(p.E, P));
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   few_route(p, r, blockIdx.x == 0, scratch);
   const int n_act = *r.n_act;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  const int64_t units = static_cast<int64_t>(n_act) * p.F + p.Fs;
-  int64_t u = units * blockIdx.x / gridDim.x;
-  const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const UpPlan plan = up_plan(p, n_act);
+  int tile = blockIdx.x;
   const int chunks = p.H / 64;
-  const int steps = (chunks + kFewWarps - 1) / kFewWarps;
+  const int rounds = (chunks + kFewWarps * kDepth - 1) / (kFewWarps * kDepth);
 
-  auto load = [&](FewA& a, const UpTile& t, int step) {
+  auto load = [&](FewStep& st, const UpTile& t, int step) {
     const int c = step * kFewWarps + warp;
     const bool on = t.gate != nullptr && c < chunks;
-    const __nv_bfloat16* base = t.gate + static_cast<int64_t>(c) * 64 + q * 16;
+    const int kofs = c * 64 + q * 16;
+    const __nv_bfloat16* base = t.gate + kofs;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int row = g + 8 * half;
       const __nv_bfloat16* pr = base + static_cast<int64_t>(row) * p.H;
       const bool have = on && row < t.rows;
-      few_ldw(a.v[0][half], pr, have);
-      few_ldw(a.v[1][half], pr + t.up, have);
+      few_ldw(st.a.v[0][half], pr, have, t.policy);
+      few_ldw(st.a.v[1][half], pr + t.up, have, t.policy);
     }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) st.b[s] = few_ldx(t.x0 + kofs + 8 * s, on && t.x0 != nullptr);
   };
 
-  UpTile cur = up_tile(p, r, n_act, u, u1);
-  FewA a0, a1;
-  load(a0, cur, 0);
+  UpTile cur = up_tile(p, r, plan, n_act, tile);
+  FewStep st[kDepth];
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) load(st[d], cur, d);
+  int flip = 0;
   while (cur.gate != nullptr) {
-    u += cur.rows;
-    const UpTile next = up_tile(p, r, n_act, u, u1);
+    tile += gridDim.x;
+    const UpTile next = up_tile(p, r, plan, n_act, tile);
     const int nt = (cur.n + 7) >> 3;
     const __nv_bfloat16* xr[NT];
+    xr[0] = nullptr;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+    for (int j = 1; j < NT; ++j) {
       const int c = j * 8 + g;
-      xr[j] = c < cur.n ? p.x + static_cast<int64_t>(cur.off < 0 ? c : r.tok[cur.off + c]) * p.H
-                        : nullptr;
+      xr[j] = c < cur.n
+                  ? p.x + static_cast<int64_t>(cur.t0 >= 0 ? cur.t0 + c : r.tok[cur.off + c]) * p.H
+                  : nullptr;
     }
-    float acc[2][NT][4];
+    float acc[NT][2][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-    for (int step = 0; step < steps; ++step) {
-      const bool last = step + 1 == steps;
-      load(a1, last ? next : cur, last ? 0 : step + 1);
-      const int c = step * kFewWarps + warp;
-      few_mul<NT>(acc, a0, xr, nt, c * 64 + q * 16, p.H);
-      a0 = a1;
+        for (int i = 0; i < 4; ++i) acc[j][m][i] = 0.0f;
+    for (int round = 0; round < rounds; ++round) {
+      const bool last = round + 1 == rounds;
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        const int step = round * kDepth + d;
+        const int c = step * kFewWarps + warp;
+        if (c < chunks) few_step<NT>(acc, st[d], nt, xr, c * 64 + q * 16, true);
+        if (last)
+          load(st[d], next, d);
+        else
+          load(st[d], cur, step + kDepth);
+      }
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       if (j < nt) {
-        float4* dst = red + ((warp * NT + j) * 2) * 32 + lane;
-        dst[0] = make_float4(acc[0][j][0], acc[0][j][1], acc[0][j][2], acc[0][j][3]);
-        dst[32] = make_float4(acc[1][j][0], acc[1][j][1], acc[1][j][2], acc[1][j][3]);
-      }
-    __syncthreads();
-    // value (lane l, register i) of a tile: row l/4 + 8*(i/2), token 2*(l%4) + i%2
-    const float* rf = reinterpret_cast<const float*>(red);
-    for (int i = threadIdx.x; i < nt * 128; i += kFewThreads) {
-      const int j = i >> 7, l = (i >> 2) & 31, v = i & 3;
-      const int row = (l >> 2) + 8 * (v >> 1);
-      const int col = j * 8 + 2 * (l & 3) + (v & 1);
-      if (row < cur.rows && col < cur.n) {
-        float gs = 0.0f, us = 0.0f;
+        float* buf = red + flip * (kFewWarps * 256);
+        flip ^= 1;
+        float4* dst = reinterpret_cast<float4*>(buf) + warp * 64 + lane;
+        dst[0] = make_float4(acc[j][0][0], acc[j][0][1], acc[j][0][2], acc[j][0][3]);
+        dst[32] = make_float4(acc[j][1][0], acc[j][1][1], acc[j][1][2], acc[j][1][3]);
+        __syncthreads();
+        // value (lane l, register v): row l/4 + 8*(v/2), token 2*(l%4) + v%2
+        const int i = threadIdx.x;
+        const int l = (i >> 2) & 31, v = i & 3;
+        const int row = (l >> 2) + 8 * (v >> 1);
+        const int col = j * 8 + 2 * (l & 3) + (v & 1);
+        if (i < 128 && row < cur.rows && col < cur.n) {
+          float gs = 0.0f, us = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
-          const float* s = rf + ((w * NT + j) * 2) * 128 + (i & 127);
-          gs += s[0];
-          us += s[128];
+          for (int w = 0; w < kFewWarps; ++w) {
+            gs += buf[w * 256 + i];
+            us += buf[w * 256 + 128 + i];
+          }
+          const __nv_bfloat16 hv = __float2bfloat16(few_silu(gs) * us);
+          if (cur.t0 >= 0)
+            p.hs[static_cast<int64_t>(cur.t0 + col) * p.Fs + cur.f0 + row] = hv;
+          else
+            p.h[static_cast<int64_t>(cur.off + col) * p.F + cur.f0 + row] = hv;
         }
-        const __nv_bfloat16 hv = __float2bfloat16(few_silu(gs) * us);
-        if (cur.off < 0)
-          p.hs[static_cast<int64_t>(col) * p.Fs + cur.f0 + row] = hv;
-        else
-          p.h[static_cast<int64_t>(cur.off + col) * p.F + cur.f0 + row] = hv;
       }
-    }
-    __syncthreads();
     cur = next;
   }
 }
@@ -398,128 +507,212 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_up_kernel(const FewParams 
 // ---------------------------------------------------------------------------
 // Kernel 2: out = residual + sum over the experts of weight * (Wd h).
 // CTA c owns an equal share of the H output rows, for every expert, so a
-// token's sum over its experts stays in one CTA. The (expert, 64-wide chunk)
-// items are split evenly over the warps; a warp adds its weighted sums into
-// its own fp32 table [token][row] in shared memory, and the tables are added
-// in warp order at the end: no atomics, the same bits every time.
+// token's sum over its experts stays in one CTA. The (expert, chunk of k) items
+// are split evenly over the warps; at an expert's end a warp adds its weighted
+// sums into its own fp32 table [token][row] in shared memory, and the tables are
+// added in warp order at the end: no atomics, the same bits every time.
+// kSpan 1: 32 rows x 64 k an item; 2: 16 rows x 128 k (a share of at most 16
+// rows would leave half of the wide item's loads empty).
 // ---------------------------------------------------------------------------
-struct DownItem {
-  const __nv_bfloat16* w;  // row 0 of this CTA's rows, at the item's chunk; null: none
-  int64_t ld;
-  int a;                   // active expert, n_act = the shared expert
-  int c;                   // chunk
+// A warp's walk over its items: first its share of the groups' items, then its
+// share of the shared expert's.
+struct DownWalk {
+  int left;                // items left, this one included
+  int a;                   // group; from n_act on: the shared expert's groups
+  int k, K;                // first k of the item; the expert's inner size
+  int n;                   // tokens of the group
+  const __nv_bfloat16* w;  // the CTA's first row, at k
+  const __nv_bfloat16* h;  // the group's first row, at k
 };
 
-template <int NT>
-__global__ void __launch_bounds__(kFewThreads, 2) few_down_kernel(const FewParams p) {
+struct DownSpan {
+  int r0, r1, s0, s1;  // the warp's items of the routed and of the shared experts
+  int chF, chS;        // items of a group
+};
+
+template <int kWide>
+__device__ __forceinline__ void down_enter(const FewParams& p, const FewRoute& r, int n_act, int rb, int a,
+                                           int c, DownWalk& d) {
+  d.a = a;
+  d.k = c * kWide;
+  if (a < n_act) {
+    const int off = r.act_off[a];
+    d.K = p.F;
+    d.n = r.act_off[a + 1] - off;
+    d.w = p.w_down + (static_cast<int64_t>(r.act_e[a]) * p.H + rb) * p.F + d.k;
+    d.h = p.h + static_cast<int64_t>(off) * p.F + d.k;
+  } else {
+    const int t0 = (a - n_act) * kFewGroup;
+    d.K = p.Fs;
+    d.n = min(kFewGroup, p.T - t0);
+    d.w = p.ws_down + static_cast<int64_t>(rb) * p.Fs + d.k;
+    d.h = p.hs + static_cast<int64_t>(t0) * p.Fs + d.k;
+  }
+}
+
+template <int kWide>
+__device__ __forceinline__ void down_start(const FewParams& p, const FewRoute& r, int n_act, int rb,
+                                           const DownSpan& s, DownWalk& d) {
+  d.left = s.r1 - s.r0 + s.s1 - s.s0;
+  d.a = 0;
+  d.k = 0;
+  d.K = 1;
+  d.n = 0;
+  d.w = d.h = nullptr;
+  if (d.left <= 0) return;
+  if (s.r1 > s.r0)
+    down_enter<kWide>(p, r, n_act, rb, s.r0 / s.chF, s.r0 % s.chF, d);
+  else
+    down_enter<kWide>(p, r, n_act, rb, n_act + s.s0 / s.chS, s.s0 % s.chS, d);
+}
+
+template <int kWide>
+__device__ __forceinline__ void down_next(const FewParams& p, const FewRoute& r, int n_act, int rb,
+                                          const DownSpan& s, DownWalk& d) {
+  if (--d.left <= 0) return;
+  if (d.left == s.s1 - s.s0 && s.r1 > s.r0) {  // on to the shared expert
+    down_enter<kWide>(p, r, n_act, rb, n_act + s.s0 / s.chS, s.s0 % s.chS, d);
+    return;
+  }
+  d.k += kWide;
+  d.w += kWide;
+  d.h += kWide;
+  if (d.k >= d.K) down_enter<kWide>(p, r, n_act, rb, d.a + 1, 0, d);
+}
+
+template <int NT, int kSpan>
+__global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(const FewParams p) {
+  constexpr int kRows = 32 / kSpan;  // rows of a pass
+  constexpr int kPitch = kRows + 8;  // of the table: 8 rows x 4 tokens in different banks
+  constexpr int kWide = 64 * kSpan;
   extern __shared__ __align__(16) uint8_t few_smem[];
-  __shared__ int scratch[kFewWarps];
   const int P = p.T * p.k;
   const FewRoute r = few_route_layout(few_smem, p.E, P);
-  float* table = reinterpret_cast<float*>(few_smem + few_route_bytes(p.E, P));
+  float* table = reinterpret_cast<float*>(few_smem + few_list_bytes(p.E, P));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  constexpr int kRows = 32;
-  constexpr int TP = NT * 8;
-  float* mine = table + warp * TP * kRows;
-
-  few_route(p, r, false, scratch);
-  const int n_act = *r.n_act;
+  const int TP = (p.T + 7) & ~7;
+  float* mine = table + warp * TP * kPitch;
   const int row0 = static_cast<int>(static_cast<int64_t>(p.H) * blockIdx.x / gridDim.x);
   const int row1 = static_cast<int>(static_cast<int64_t>(p.H) * (blockIdx.x + 1) / gridDim.x);
-  const int chF = p.F / 64, chS = p.Fs / 64;
-  const int items = n_act * chF + chS;
-  const int i0 = static_cast<int>(static_cast<int64_t>(items) * warp / kFewWarps);
-  const int i1 = static_cast<int>(static_cast<int64_t>(items) * (warp + 1) / kFewWarps);
-  bool waited = false;
 
-  for (int rb = row0; rb < row1; rb += kRows) {
-    const int rows = min(kRows, row1 - rb);
-    for (int i = lane; i < TP * kRows; i += 32) mine[i] = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1 has ended
+  few_route_load(p, r);
+  const int n_act = *r.n_act;
+  DownSpan sp;
+  sp.chF = (p.F + kWide - 1) / kWide;
+  sp.chS = (p.Fs + kWide - 1) / kWide;
+  const int routed = n_act * sp.chF, shared = sp.chS * ((p.T + kFewGroup - 1) / kFewGroup);
+  sp.r0 = static_cast<int>(static_cast<int64_t>(routed) * warp / kFewWarps);
+  sp.r1 = static_cast<int>(static_cast<int64_t>(routed) * (warp + 1) / kFewWarps);
+  sp.s0 = shared * warp / kFewWarps;
+  sp.s1 = shared * (warp + 1) / kFewWarps;
+  // several groups read the shared expert's rows, or a busy expert's
+  const uint64_t policy = p.T > kFewGroup ? l2_policy_evict_normal() : l2_policy_evict_first();
+
+  // even passes: 49 rows are 25 and 24, not 32 and 17
+  const int passes = (row1 - row0 + kRows - 1) / kRows;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int rb = row0 + (row1 - row0) * pass / passes;
+    const int rows = row0 + (row1 - row0) * (pass + 1) / passes - rb;
+    for (int i = lane; i < TP * kPitch; i += 32) mine[i] = 0.0f;
     __syncwarp();
-    auto item = [&](int i) {
-      DownItem d;
-      d.w = nullptr;
-      d.ld = p.F;
-      d.a = -1;
-      d.c = 0;
-      if (i >= i1) return d;
-      if (i < n_act * chF) {
-        d.a = i / chF;
-        d.c = i - d.a * chF;
-        d.w = p.w_down + (static_cast<int64_t>(r.act_e[d.a]) * p.H + rb) * p.F + d.c * 64;
-      } else {
-        d.a = n_act;
-        d.c = i - n_act * chF;
-        d.ld = p.Fs;
-        d.w = p.ws_down + static_cast<int64_t>(rb) * p.Fs + d.c * 64;
-      }
-      return d;
-    };
-    auto load = [&](FewA& a, const DownItem& d) {
+    // weights of an item: kSpan 1: block m = rows 16m..; kSpan 2: block m = k 64m..
+    auto load = [&](FewA& a, uint4 (&b)[2 * kSpan], const DownWalk& d) {
+      const bool on = d.left > 0;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int row = 16 * m + 8 * half + g;
-          const bool have = d.w != nullptr && row < rows;
-          few_ldw(a.v[m][half], d.w + row * d.ld + q * 16, have);
+          const int row = (kSpan == 1 ? 16 * m : 0) + 8 * half + g;
+          const int k = (kSpan == 1 ? 0 : 64 * m) + q * 16;
+          few_ldw(a.v[m][half], d.w + static_cast<int64_t>(row) * d.K + k,
+                  on && row < rows && (kSpan == 1 || d.k + k < d.K), policy);
+        }
+#pragma unroll
+      for (int i = 0; i < kSpan; ++i)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int k = 64 * i + q * 16 + 8 * s;
+          b[2 * i + s] = few_ldx(d.h + static_cast<int64_t>(g) * d.K + k,
+                                 on && g < d.n && (kSpan == 1 || d.k + k < d.K));
         }
     };
-    float acc[2][NT][4];
+    float acc[NT][2][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-    DownItem cur = item(i0);
-    FewA a0, a1;
-    load(a0, cur);
-    if (!waited) {
-      // the weights are on their way; h comes from kernel 1
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      waited = true;
+        for (int i = 0; i < 4; ++i) acc[j][m][i] = 0.0f;
+    FewA aw[kDepth];
+    uint4 bh[kDepth][2 * kSpan];
+    DownWalk cur, ahead;
+    down_start<kWide>(p, r, n_act, rb, sp, cur);
+    ahead = cur;
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      load(aw[d], bh[d], ahead);
+      down_next<kWide>(p, r, n_act, rb, sp, ahead);
     }
-    for (int i = i0; i < i1; ++i) {
-      const DownItem next = item(i + 1);
-      load(a1, next);
-      const bool shared = cur.a == n_act;
-      const int off = shared ? 0 : r.act_off[cur.a];
-      const int n = shared ? p.T : r.act_off[cur.a + 1] - off;
-      const int nt = (n + 7) >> 3;
-      const __nv_bfloat16* xr[NT];
+    while (cur.left > 0) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int c = j * 8 + g;
-        xr[j] = c < n ? (shared ? p.hs + static_cast<int64_t>(c) * p.Fs
-                                : p.h + static_cast<int64_t>(off + c) * p.F)
-                      : nullptr;
-      }
-      few_mul<NT>(acc, a0, xr, nt, cur.c * 64 + q * 16, static_cast<int>(cur.ld));
-      if (next.a != cur.a) {
-        // the expert ends here (or its other chunks are another warp's)
+      for (int d = 0; d < kDepth; ++d) {
+        if (cur.left > 0) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          if (j < nt) {
+          for (int j = 0; j < NT; ++j)
+            if (j * 8 < cur.n) {
+              const bool have = j > 0 && j * 8 + g < cur.n;
+              const __nv_bfloat16* hr = cur.h + static_cast<int64_t>(j * 8 + g) * cur.K;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const int col = j * 8 + 2 * q + (v & 1);
-              if (col < n) {
-                const int t = shared ? col : r.tok[off + col];
-                const float w = shared ? 1.0f : p.scale * r.weight[off + col];
+              for (int z = 0; z < kSpan; ++z)
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-                  mine[t * kRows + 16 * m + 8 * (v >> 1) + g] += w * acc[m][j][v];
-              }
-              acc[0][j][v] = 0.0f;
-              acc[1][j][v] = 0.0f;
+                for (int s = 0; s < 2; ++s) {
+                  const int k = 64 * z + q * 16 + 8 * s;
+                  const uint4 b = j == 0 ? bh[d][2 * z + s]
+                                         : few_ldx(hr + k, have && (kSpan == 1 || cur.k + k < cur.K));
+#pragma unroll
+                  for (int m = 0; m < 2; ++m)
+                    if (kSpan == 1 || m == z) {
+                      const uint32_t* lo = aw[d].v[m][0].r + 4 * s;
+                      const uint32_t* hi = aw[d].v[m][1].r + 4 * s;
+                      few_mma(acc[j][m], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+                      few_mma(acc[j][m], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+                    }
+                }
             }
+          if (cur.k + kWide >= cur.K || cur.left == 1 || cur.left == sp.s1 - sp.s0 + 1) {
+            // the group ends here (or its other items are another warp's)
+            const bool routed_group = cur.a < n_act;
+            const int off = routed_group ? r.act_off[cur.a] : (cur.a - n_act) * kFewGroup;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              if (j * 8 < cur.n) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  const int col = j * 8 + 2 * q + (v & 1);
+                  if (col < cur.n) {
+                    const int t = routed_group ? r.tok[off + col] : off + col;
+                    const float w = routed_group ? p.scale * r.weight[off + col] : 1.0f;
+                    float* cell = mine + t * kPitch + 8 * (v >> 1) + g;
+                    if (kSpan == 1) {
+                      cell[0] += w * acc[j][0][v];
+                      cell[16] += w * acc[j][1][v];
+                    } else {
+                      cell[0] += w * (acc[j][0][v] + acc[j][1][v]);
+                    }
+                  }
+                  acc[j][0][v] = 0.0f;
+                  acc[j][1][v] = 0.0f;
+                }
+              }
+            __syncwarp();
           }
-        __syncwarp();
+          down_next<kWide>(p, r, n_act, rb, sp, cur);
+        }
+        load(aw[d], bh[d], ahead);
+        down_next<kWide>(p, r, n_act, rb, sp, ahead);
       }
-      cur = next;
-      a0 = a1;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < p.T * kRows; i += kFewThreads) {
@@ -527,7 +720,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_down_kernel(const FewParam
       if (row < rows) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) s += table[(w * TP + t) * kRows + row];
+        for (int w = 0; w < kFewWarps; ++w) s += table[(w * TP + t) * kPitch + row];
         const int64_t at = static_cast<int64_t>(t) * p.H + rb + row;
         if (p.residual != nullptr) s += __bfloat162float(p.residual[at]);
         p.out[at] = __float2bfloat16(s);
@@ -535,50 +728,59 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_down_kernel(const FewParam
     }
     __syncthreads();
   }
-  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename K>
+cudaError_t few_launch(K kernel, const FewParams& p, size_t smem, bool early,
+                       cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count()));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int NT>
 cudaError_t run_few(const FewParams& p, cudaStream_t stream) {
-  const size_t route = few_route_bytes(p.E, p.T * p.k);
-  const size_t up_smem = route + sizeof(float4) * kFewWarps * NT * 2 * 32;
-  const size_t down_smem = route + sizeof(float) * kFewWarps * NT * 8 * 32;
+  auto up = few_up_kernel<NT>;
+  auto wide = few_down_kernel<NT, 1>;
+  auto narrow = few_down_kernel<NT, 2>;
+  const int E = p.E, P = p.T * p.k;
+  const size_t up_smem = few_route_bytes(E, P) + 2 * kFewWarps * 256 * sizeof(float);
+  const size_t rows = static_cast<size_t>(kFewWarps) * ((p.T + 7) & ~7) * sizeof(float);
+  const size_t wide_smem = few_list_bytes(E, P) + rows * 40, narrow_smem = few_list_bytes(E, P) + rows * 24;
   static bool set[64] = {};  // the attributes hold for the process: once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!set[dev]) {
-    const size_t most = few_route_bytes(1024, 32 * NT * 8);
-    e = cudaFuncSetAttribute(few_up_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(most + up_smem - route));
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(few_down_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(most + down_smem - route));
-    if (e != cudaSuccess) return e;
+    const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const int most = 224 * 1024;  // the largest problem (64 tokens, k 32, 1024 experts) takes 196 KB
+    if ((e = cudaFuncSetAttribute(up, a, most)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(wide, a, most)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(narrow, a, most)) != cudaSuccess) return e;
     set[dev] = true;
   }
-  const int grid = 2 * device_sm_count();
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = up_smem;
-  cfg.stream = stream;
-  e = cudaLaunchKernelEx(&cfg, few_up_kernel<NT>, p);
+  e = few_launch(up, p, up_smem, false, stream);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.dynamicSmemBytes = down_smem;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_down_kernel<NT>, p);
+  const int share = (p.H + device_sm_count() - 1) / device_sm_count();  // output rows of a block
+  return share > 16 ? few_launch(wide, p, wide_smem, true, stream)
+                    : few_launch(narrow, p, narrow_smem, true, stream);
 }
 
 }  // namespace
 
+size_t few_list_bytes_of(int E, int P) { return few_list_bytes(E, P); }
+
 cudaError_t launch_few(const FewLaunch& L, cudaStream_t stream) {
-  FewParams p;
+  FewParams p = {};
   p.T = L.T;
   p.H = L.H;
   p.F = L.F;
@@ -601,10 +803,9 @@ cudaError_t launch_few(const FewLaunch& L, cudaStream_t stream) {
   p.hs = static_cast<__nv_bfloat16*>(L.hs);
   p.out = static_cast<__nv_bfloat16*>(L.out);
   p.status = L.status;
+  p.list = static_cast<uint4*>(L.list);
   if (p.T <= 8) return run_few<1>(p, stream);
-  if (p.T <= 16) return run_few<2>(p, stream);
-  if (p.T <= 32) return run_few<4>(p, stream);
-  return run_few<8>(p, stream);
+  return run_few<2>(p, stream);
 }
 
 }  // namespace moe

@@ -30,18 +30,18 @@ __device__ __forceinline__ void few_mma(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 
 // 32 bytes of a weight row (four lanes take a whole 128-byte line): read once by
-// one lane, so it is kept out of L1 and goes first when L2 needs room. A row
+// one lane, so it is kept out of L1; `policy` says what L2 does with it. A row
 // that is not there reads as zero.
 struct FewW {
   uint32_t r[8];
 };
-__device__ __forceinline__ void few_ldw(FewW& v, const __nv_bfloat16* p, bool on) {
+__device__ __forceinline__ void few_ldw(FewW& v, const __nv_bfloat16* p, bool on, uint64_t policy) {
   if (on) {
     asm volatile(
-        "ld.global.nc.L1::no_allocate.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        "ld.global.nc.L1::no_allocate.L2::cache_hint.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
         : "=r"(v.r[0]), "=r"(v.r[1]), "=r"(v.r[2]), "=r"(v.r[3]), "=r"(v.r[4]), "=r"(v.r[5]),
           "=r"(v.r[6]), "=r"(v.r[7])
-        : "l"(p));
+        : "l"(p), "l"(policy));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v.r[i] = 0u;

@@ -157,9 +157,11 @@ struct FewLaunch {
   const void* residual = nullptr;
   void* h = nullptr;   // bf16 [T*k, F]
   void* hs = nullptr;  // bf16 [T, F_shared]
+  void* list = nullptr;  // few_list_bytes_of(E, T * k) bytes, 16-byte aligned
   void* out = nullptr;
   int32_t* status = nullptr;
 };
+size_t few_list_bytes_of(int E, int P);
 cudaError_t launch_few(const FewLaunch& L, cudaStream_t stream);
 
 // Layer norm (norm.cu). Row pitches in elements.

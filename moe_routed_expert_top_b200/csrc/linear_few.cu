@@ -18,6 +18,7 @@
 #include "few.cuh"
 #include "internal.h"
 #include "linear.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 
@@ -29,14 +30,16 @@ struct LinearFewParams {
   const __nv_bfloat16* x;
   const __nv_bfloat16* w;
   LinearEpilogue e;
+  int32_t* status;
 };
 
 // 16 values of a weight row from k on; kWhole: 32-byte aligned and K % 16 == 0,
 // else two 16-byte loads (K % 8 == 0).
 template <bool kWhole>
-__device__ __forceinline__ void linear_ldw(FewW& v, const __nv_bfloat16* row, int k, int K, bool on) {
+__device__ __forceinline__ void linear_ldw(FewW& v, const __nv_bfloat16* row, int k, int K, bool on,
+                                           uint64_t policy) {
   if constexpr (kWhole) {
-    few_ldw(v, row + k, on && k < K);
+    few_ldw(v, row + k, on && k < K, policy);
   } else {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -65,12 +68,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const Linear
   const int row1 = static_cast<int>(static_cast<int64_t>(p.N) * (blockIdx.x + 1) / gridDim.x);
   const int steps = (p.K + kFewWarps * kSpan - 1) / (kFewWarps * kSpan);
   const int nt = (p.M + 7) >> 3;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing here waits on a barrier in memory
 
   const __nv_bfloat16* xr[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
     xr[j] = j * 8 + g < p.M ? p.x + static_cast<int64_t>(j * 8 + g) * p.ldx : nullptr;
 
+  const uint64_t policy = l2_policy_evict_first();
   auto load = [&](FewA& a, int rb, int step) {
     const int k0 = (step * kFewWarps + warp) * kSpan + q * 16;
 #pragma unroll
@@ -79,7 +84,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const Linear
       for (int half = 0; half < 2; ++half) {
         const int row = rb + g + (kTall ? 16 * m + 8 * half : 0);
         const int k = k0 + (kTall ? 0 : 64 * (2 * m + half));
-        linear_ldw<kWhole>(a.v[m][half], p.w + static_cast<int64_t>(row) * p.ldw, k, p.K, row < row1);
+        linear_ldw<kWhole>(a.v[m][half], p.w + static_cast<int64_t>(row) * p.ldw, k, p.K, row < row1,
+                           policy);
       }
   };
 
@@ -184,6 +190,7 @@ cudaError_t launch_linear_few(const LinearLaunch& L, cudaStream_t stream) {
   p.x = static_cast<const __nv_bfloat16*>(L.A);
   p.w = static_cast<const __nv_bfloat16*>(L.B);
   p.e = L.e;
+  p.status = L.status;
   if (p.M <= 8) return run_few<1>(p, stream);
   if (p.M <= 16) return run_few<2>(p, stream);
   if (p.M <= 32) return run_few<4>(p, stream);
