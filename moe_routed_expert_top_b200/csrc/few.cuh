@@ -60,28 +60,4 @@ struct FewA {
   FewW v[2][2];  // [block][row half]
 };
 
-// acc[block][token tile] += A * B over the chunk, B's words loaded from the
-// lane's token row of each tile (null: no such token) while they lie before K.
-template <int NT>
-__device__ __forceinline__ void few_mul(float (&acc)[2][NT][4], const FewA& a,
-                                        const __nv_bfloat16* const (&xr)[NT], int nt, int kofs,
-                                        int K) {
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    if (j < nt) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint4 b = few_ldx(xr[j] + kofs + 8 * s, xr[j] != nullptr && kofs + 8 * s < K);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint32_t* lo = a.v[m][0].r + 4 * s;
-          const uint32_t* hi = a.v[m][1].r + 4 * s;
-          few_mma(acc[m][j], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-          few_mma(acc[m][j], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
-        }
-      }
-    }
-  }
-}
-
 }  // namespace moe

@@ -37,6 +37,7 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "internal.h"
 #include "linear.cuh"
@@ -54,7 +55,7 @@ struct LinParams {
   int kb_total, kb_split;  // 64-wide k blocks: all, and of one split
   float* partial;          // [splits][M][N] when splits > 1
   int32_t* status;
-  int wide;                // 32-byte stores of y are possible
+  int wide;                // every row of y, z, residual (and partial) takes 32-byte accesses
   LinearEpilogue e;
 };
 
@@ -63,11 +64,13 @@ struct LCfg {
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = (BN / 2) * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int STAGES = BN == 256 ? 5 : 7;
   static constexpr int NUM_ACC = 2;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * NUM_ACC + 1;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NUM_BARS * 8 + 32;
+  // each epilogue warp's 32 x 32 block, its rows 33 apart
+  static constexpr int BLOCK_BYTES = 32 * 33 * 4;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 8 * BLOCK_BYTES + NUM_BARS * 8 + 32;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -96,6 +99,80 @@ __device__ __forceinline__ void lin_decode(const LinParams& p, int t, int& tm, i
   tm = 8 * band + (r - tn * h);
 }
 
+__device__ __forceinline__ void lin_st8(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void lin_ld8(uint32_t* v, const void* p) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void lin_store32_f32(float* dst, const uint32_t (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) lin_st8(dst + i, v + i);
+}
+__device__ __forceinline__ void lin_store32_bf16(__nv_bfloat16* dst, const uint32_t (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 16) {
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      o[j] = pack_bf16x2(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
+    lin_st8(dst + i, o);
+  }
+}
+
+template <int kAct>
+__device__ __forceinline__ void lin_act32(uint32_t (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(linear_act(__uint_as_float(v[i]), kAct));
+}
+
+// The epilogue of 32 columns n.. of row m, all accesses 32 bytes wide.
+__device__ __forceinline__ void lin_store32(const LinearEpilogue& e, long long m, int n, uint32_t (&v)[32]) {
+  if (e.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + linear_bias(e, n + i));
+  }
+  if (e.z != nullptr) lin_store32_bf16(static_cast<__nv_bfloat16*>(e.z) + m * e.ldz + n, v);
+  if (e.act == kActRelu)
+    lin_act32<kActRelu>(v);
+  else if (e.act == kActSilu)
+    lin_act32<kActSilu>(v);
+  else if (e.act == kActGelu)
+    lin_act32<kActGelu>(v);
+  if (e.res != nullptr) {
+    uint32_t r[8];
+    if (e.res_f32) {
+      const float* src = static_cast<const float*>(e.res) + m * e.ldr + n;
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        lin_ld8(r, src + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[i + j] = __float_as_uint(__uint_as_float(v[i + j]) + __uint_as_float(r[j]));
+      }
+    } else {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.res) + m * e.ldr + n;
+#pragma unroll
+      for (int i = 0; i < 32; i += 16) {
+        lin_ld8(r, src + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[i + 2 * j] = __float_as_uint(__uint_as_float(v[i + 2 * j]) + bf16lo_to_f32(r[j]));
+          v[i + 2 * j + 1] = __float_as_uint(__uint_as_float(v[i + 2 * j + 1]) + bf16hi_to_f32(r[j]));
+        }
+      }
+    }
+  }
+  if (e.y_f32)
+    lin_store32_f32(static_cast<float*>(e.y) + m * e.ldy + n, v);
+  else
+    lin_store32_bf16(static_cast<__nv_bfloat16*>(e.y) + m * e.ldy + n, v);
+}
+
 template <bool AMN, bool BMN, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -109,7 +186,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * Cfg::A_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sB + STAGES * Cfg::B_BYTES);
+  float* sBlock = reinterpret_cast<float*>(sB + STAGES * Cfg::B_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sBlock) + 8 * Cfg::BLOCK_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -271,11 +349,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    // Group g takes the tile's columns [g BN/2, (g+1) BN/2); a thread has one
-    // row, in runs of 32 columns.
+    // Group g takes the tile's columns [g BN/2, (g+1) BN/2) in runs of 32; a
+    // warp has 32 rows. Tensor memory gives a thread 32 columns of one row.
+    //   32-byte accesses possible: it stores them as they are (32 rows at a time,
+    //     whole sectors);
+    //   else (odd pitches, the last columns): through shared memory, so that the
+    //     lanes lie along the row (a 2-byte store to 32 rows at a time would cost
+    //     more than the main loop).
     const int grp = (warp - 2) >> 2;
     const int q = warp & 3;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    float* block = sBlock + (warp - 2) * (32 * 33);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = pair; t < items; t += npairs) {
@@ -286,42 +370,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got) break;
       tc_fence_after();
-      const long long m = static_cast<long long>(tm) * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const long long m0 = static_cast<long long>(tm) * 256 + static_cast<int>(rank) * 128 + q * 32;
+      const int rows = static_cast<int>(min(32ll, p.M - m0));
       const int c0 = tn * BN + grp * (BN / 2);
 #pragma unroll 1
       for (int j = 0; j < BN / 2; j += 32) {
+        const int n = c0 + j;
+        if (rows <= 0 || n >= p.N) break;
         uint32_t v[32];
         tmem_ld32(lane_base + static_cast<uint32_t>(acc * BN + grp * (BN / 2) + j), v);
         tmem_ld_wait();
-        const int n = c0 + j;
-        if (m < p.M && n < p.N) {
-          const int cols = min(32, p.N - n);
-          if (p.splits > 1) {
-            float* dst = p.partial + (static_cast<long long>(sp) * p.M + m) * p.N + n;
-            if (cols == 32 && (p.N & 3) == 0) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < cols) dst[i] = __uint_as_float(v[i]);
-            }
-          } else if (cols == 32 && p.wide && p.e.res == nullptr && p.e.z == nullptr &&
-                     p.e.act == kActNone && p.e.bias == nullptr && !p.e.y_f32) {
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.e.y) + m * p.e.ldy + n;
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(dst + i) = make_uint4(
-                  pack_bf16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
-                  pack_bf16x2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])),
-                  pack_bf16x2(__uint_as_float(v[i + 4]), __uint_as_float(v[i + 5])),
-                  pack_bf16x2(__uint_as_float(v[i + 6]), __uint_as_float(v[i + 7])));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < cols) linear_store(p.e, m, n + i, __uint_as_float(v[i]));
+        const int cols = min(32, p.N - n);
+        if (p.wide && cols == 32) {
+          if (lane < rows) {
+            if (p.splits > 1)
+              lin_store32_f32(p.partial + (static_cast<long long>(sp) * p.M + m0 + lane) * p.N + n, v);
+            else
+              lin_store32(p.e, m0 + lane, n, v);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) block[lane * 33 + i] = __uint_as_float(v[i]);
+          __syncwarp();
+          if (lane < cols) {
+            if (p.splits > 1) {
+              float* dst = p.partial + (static_cast<long long>(sp) * p.M + m0) * p.N + n + lane;
+              for (int i = 0; i < rows; ++i) dst[static_cast<long long>(i) * p.N] = block[i * 33 + lane];
+            } else {
+              const float bias = linear_bias(p.e, n + lane);
+              for (int i0 = 0; i0 < rows; i0 += 8) {
+                float res[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  res[i] = p.e.res != nullptr && i0 + i < rows ? linear_res(p.e, m0 + i0 + i, n + lane) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (i0 + i < rows) {
+                    float z;
+                    const float y = linear_result(p.e, block[(i0 + i) * 33 + lane], bias, res[i], &z);
+                    linear_put(p.e, m0 + i0 + i, n + lane, y, z);
+                  }
+              }
+            }
+          }
+          __syncwarp();
         }
       }
       tc_fence_before();
@@ -343,45 +435,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   }
 }
 
-// y from the splits' sums, in split order.
+// y from the splits' sums, in split order. A block has 64 columns x 4 rows.
 __global__ void __launch_bounds__(256) linear_join_kernel(const float* partial, int splits, int M, int N,
                                                           const LinearEpilogue e) {
+  const int n = blockIdx.x * 64 + threadIdx.x;
+  if (n >= N) return;
   const long long total = static_cast<long long>(M) * N;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    float s = partial[i];
-    for (int k = 1; k < splits; ++k) s += partial[k * total + i];
-    const long long m = i / N;
-    linear_store(e, m, static_cast<int>(i - m * N), s);
+  const float bias = linear_bias(e, n);
+  for (long long m = blockIdx.y * 4 + threadIdx.y; m < M; m += gridDim.y * 4) {
+    const float* src = partial + m * N + n;
+    const float res = e.res != nullptr ? linear_res(e, m, n) : 0.0f;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < splits; ++k) s += src[k * total];
+    float z;
+    const float y = linear_result(e, s, bias, res, &z);
+    linear_put(e, m, n, y, z);
   }
 }
 
 // dz = dy * act'(z), rounded to bf16 (the MMA's operand type; dbias takes the
-// unrounded values), and the column sums of a block's rows. A warp has 32 columns.
+// unrounded values), and the column sums of a block's rows. A thread has V
+// columns, a block's 8 warps every eighth row. Bound by HBM: one pass.
 constexpr int kDzRows = 64;      // rows of a block, while kDzLines blocks cover M
 constexpr int kDzLines = 1024;
+template <int V, bool kF32>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzLaunch p) {
-  __shared__ float sum[8][33];
+  using Dy = typename std::conditional<kF32, float, __nv_bfloat16>::type;
+  struct alignas(sizeof(Dy) * V > 16 ? 16 : sizeof(Dy) * V) DyV {
+    Dy v[V];
+  };
+  struct alignas(2 * V) ZV {
+    __nv_bfloat16 v[V];
+  };
+  __shared__ float sum[8][32 * V + 1];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int n = blockIdx.x * 32 + lane;
+  const int n = (blockIdx.x * 32 + lane) * V;
   const long long m0 = static_cast<long long>(p.M) * blockIdx.y / gridDim.y;
   const long long m1 = static_cast<long long>(p.M) * (blockIdx.y + 1) / gridDim.y;
-  float s = 0.0f;
-  if (n < p.N)
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = 0.0f;
+  if (n < p.N) {
+    const Dy* dy = static_cast<const Dy*>(p.dy) + n;
+    const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(p.z) + n;
+#pragma unroll 4
     for (long long m = m0 + w; m < m1; m += 8) {
-      float d = p.dy_f32 ? static_cast<const float*>(p.dy)[m * p.lddy + n]
-                         : __bfloat162float(static_cast<const __nv_bfloat16*>(p.dy)[m * p.lddy + n]);
-      if (p.z != nullptr)
-        d *= linear_slope(__bfloat162float(static_cast<const __nv_bfloat16*>(p.z)[m * p.ldz + n]), p.act);
-      if (p.dz != nullptr) static_cast<__nv_bfloat16*>(p.dz)[m * p.lddz + n] = __float2bfloat16(d);
-      s += d;
+      const DyV d = *reinterpret_cast<const DyV*>(dy + m * p.lddy);
+      float f[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = static_cast<float>(d.v[i]);
+      if (p.z != nullptr) {
+        const ZV zv = *reinterpret_cast<const ZV*>(z + m * p.ldz);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] *= linear_slope(__bfloat162float(zv.v[i]), p.act);
+      }
+      if (p.dz != nullptr) {
+        ZV o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o.v[i] = __float2bfloat16(f[i]);
+        *reinterpret_cast<ZV*>(static_cast<__nv_bfloat16*>(p.dz) + m * p.lddz + n) = o;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] += f[i];
     }
+  }
   if (p.lines == nullptr) return;
-  sum[w][lane] = s;
+#pragma unroll
+  for (int i = 0; i < V; ++i) sum[w][i * 32 + lane] = s[i];
   __syncthreads();
-  if (w == 0 && n < p.N) {
-    for (int i = 1; i < 8; ++i) s += sum[i][lane];
-    p.lines[static_cast<long long>(blockIdx.y) * p.N + n] = s;
+  for (int i = threadIdx.x; i < 32 * V; i += 256) {
+    const int c = (blockIdx.x * 32 + (i & 31)) * V + (i >> 5);
+    if (c < p.N) {
+      float t = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t += sum[j][i];
+      p.lines[static_cast<long long>(blockIdx.y) * p.N + c] = t;
+    }
   }
 }
 
@@ -475,18 +605,24 @@ cudaError_t run_gemm(const LinearLaunch& L, const LinPlan& plan, cudaStream_t st
   p.kb_split = plan.kb_split;
   p.partial = L.partial;
   p.status = L.status;
-  p.wide = L.e.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(L.e.y) & 15u) == 0;
+  if (plan.splits > 1) {
+    p.wide = L.N % 8 == 0 && (reinterpret_cast<uintptr_t>(L.partial) & 31u) == 0;
+  } else {
+    auto rows32 = [](const void* at, long long ld, int size) {
+      return at == nullptr || (ld * size % 32 == 0 && (reinterpret_cast<uintptr_t>(at) & 31u) == 0);
+    };
+    p.wide = rows32(L.e.y, L.e.ldy, L.e.y_f32 ? 4 : 2) && rows32(L.e.z, L.e.ldz, 2) &&
+             rows32(L.e.res, L.e.ldr, L.e.res_f32 ? 4 : 2);
+  }
   p.e = L.e;
   const long long items = static_cast<long long>(plan.tiles_m) * plan.tiles_n * plan.splits;
   const int pairs = items < max_pairs_cache[dev] ? static_cast<int>(items) : max_pairs_cache[dev];
   linear_gemm_kernel<AMN, BMN, BN><<<2 * pairs, kLinThreads, Cfg::SMEM_BYTES, stream>>>(tmA, tmB, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || plan.splits == 1) return e;
-  const long long total = static_cast<long long>(L.M) * L.N;
-  long long blocks = (total + 255) / 256;
-  const long long cap = static_cast<long long>(device_sm_count()) * 8;
-  linear_join_kernel<<<static_cast<unsigned>(blocks < cap ? blocks : cap), 256, 0, stream>>>(
-      L.partial, plan.splits, L.M, L.N, L.e);
+  const unsigned rows = (static_cast<unsigned>(L.M) + 3) / 4;
+  linear_join_kernel<<<dim3((static_cast<unsigned>(L.N) + 63) / 64, rows < 16384 ? rows : 16384), dim3(64, 4), 0,
+                       stream>>>(L.partial, plan.splits, L.M, L.N, L.e);
   return cudaGetLastError();
 }
 
@@ -512,11 +648,23 @@ int linear_dz_lines(int M) {
 }
 
 cudaError_t launch_linear_dz(const LinearDzLaunch& L, cudaStream_t stream) {
-  const dim3 grid((static_cast<unsigned>(L.N) + 31) / 32, static_cast<unsigned>(linear_dz_lines(L.M)));
-  linear_dz_kernel<<<grid, 256, 0, stream>>>(L);
+  const int lines = linear_dz_lines(L.M);
+  auto rows16 = [](const void* at, long long ld, int size) {
+    return at == nullptr || (ld * size % 16 == 0 && (reinterpret_cast<uintptr_t>(at) & 15u) == 0);
+  };
+  const bool wide = L.N % 8 == 0 && rows16(L.dy, L.lddy, L.dy_f32 ? 4 : 2) && rows16(L.z, L.ldz, 2) &&
+                    rows16(L.dz, L.lddz, 2);
+  const int cols = wide ? 256 : 32;
+  const dim3 grid((static_cast<unsigned>(L.N) + cols - 1) / cols, static_cast<unsigned>(lines));
+  if (wide)
+    L.dy_f32 ? linear_dz_kernel<8, true><<<grid, 256, 0, stream>>>(L)
+             : linear_dz_kernel<8, false><<<grid, 256, 0, stream>>>(L);
+  else
+    L.dy_f32 ? linear_dz_kernel<1, true><<<grid, 256, 0, stream>>>(L)
+             : linear_dz_kernel<1, false><<<grid, 256, 0, stream>>>(L);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || L.lines == nullptr) return e;
-  return launch_sum_lines(L.lines, 1, linear_dz_lines(L.M), L.N, L.dbias, nullptr, stream);
+  return launch_sum_lines(L.lines, 1, lines, L.N, L.dbias, nullptr, stream);
 }
 
 }  // namespace moe

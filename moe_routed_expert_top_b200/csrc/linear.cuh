@@ -47,21 +47,33 @@ __device__ __forceinline__ float linear_bias(const LinearEpilogue& e, int n) {
                     : __bfloat162float(static_cast<const __nv_bfloat16*>(e.bias)[n]);
 }
 
-// One value of the result: `s` = (x W^T)[m][n].
-__device__ __forceinline__ void linear_store(const LinearEpilogue& e, long long m, int n, float s) {
-  const float z = s + linear_bias(e, n);
-  if (e.z != nullptr) static_cast<__nv_bfloat16*>(e.z)[m * e.ldz + n] = __float2bfloat16(z);
-  float y = linear_act(z, e.act);
-  if (e.res != nullptr) {
-    const long long at = m * e.ldr + n;
-    y += e.res_f32 ? static_cast<const float*>(e.res)[at]
+// The result of one value, `s` = (x W^T)[m][n], whose bias is `bias` and whose
+// residual value is `res`.
+__device__ __forceinline__ float linear_result(const LinearEpilogue& e, float s, float bias, float res,
+                                               float* z) {
+  *z = s + bias;
+  return linear_act(*z, e.act) + res;
+}
+
+__device__ __forceinline__ float linear_res(const LinearEpilogue& e, long long m, int n) {
+  const long long at = m * e.ldr + n;
+  return e.res_f32 ? static_cast<const float*>(e.res)[at]
                    : __bfloat162float(static_cast<const __nv_bfloat16*>(e.res)[at]);
-  }
+}
+
+__device__ __forceinline__ void linear_put(const LinearEpilogue& e, long long m, int n, float y, float z) {
+  if (e.z != nullptr) static_cast<__nv_bfloat16*>(e.z)[m * e.ldz + n] = __float2bfloat16(z);
   const long long at = m * e.ldy + n;
   if (e.y_f32)
     static_cast<float*>(e.y)[at] = y;
   else
     static_cast<__nv_bfloat16*>(e.y)[at] = __float2bfloat16(y);
+}
+
+__device__ __forceinline__ void linear_store(const LinearEpilogue& e, long long m, int n, float s) {
+  float z;
+  const float y = linear_result(e, s, linear_bias(e, n), e.res != nullptr ? linear_res(e, m, n) : 0.0f, &z);
+  linear_put(e, m, n, y, z);
 }
 
 }  // namespace moe

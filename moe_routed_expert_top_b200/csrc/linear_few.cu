@@ -1,15 +1,14 @@
-// linear_few.cu - the linear product y = act(x W^T + bias) + residual for 1..64
+// linear_few.cu - the linear product y = act(x W^T + bias) + residual for a few
 // rows of x (a decode step's projections and router logits).
 //
 // What bounds it: the weight's N*K values, read once from HBM. The layout is the
-// few-token layer's (few.cuh): every CTA takes an equal share of the weight's
-// rows, its warps split k, their sums meet in shared memory and the epilogue
-// follows there. Two shapes of tile:
-//   32 rows x 64 k a warp and step, where a CTA has more than 8 rows;
-//   8 rows x 256 k, where it has fewer (a router: 256 rows over 296 CTAs). The
-//     wide tile would then load 128 bytes a warp and step and the time is k's
-//     length in memory latencies; with four chunks of the same rows at once it
-//     is a quarter of that.
+// few-token layer's (few.cuh, few.cu): the weight's rows are cut into equal tiles
+// over the CTAs, a CTA's eight warps split k and have kDepth steps in flight each,
+// their sums meet in shared memory and the epilogue follows there. A step of a
+// warp is always 32 row pieces of 128 bytes; their shape follows the rows that a
+// CTA gets (kSpan): 32 rows x 64 k, 16 x 128 or 8 x 256. A router has 2 rows a
+// CTA: as 32 x 64 it would load 256 bytes a step and take k's length in memory
+// latencies.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,6 +25,7 @@ namespace {
 
 struct LinearFewParams {
   int M, N, K;
+  int tiles, groups;  // row tiles; groups of NT * 8 rows of x
   long long ldx, ldw;
   const __nv_bfloat16* x;
   const __nv_bfloat16* w;
@@ -44,10 +44,10 @@ __device__ __forceinline__ void linear_ldw(FewW& v, const __nv_bfloat16* row, in
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (on && k + 8 * s < K)
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+        asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
                      : "=r"(v.r[4 * s]), "=r"(v.r[4 * s + 1]), "=r"(v.r[4 * s + 2]),
                        "=r"(v.r[4 * s + 3])
-                     : "l"(row + k + 8 * s));
+                     : "l"(row + k + 8 * s), "l"(policy));
       else
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.r[4 * s + i] = 0u;
@@ -55,133 +55,170 @@ __device__ __forceinline__ void linear_ldw(FewW& v, const __nv_bfloat16* row, in
   }
 }
 
-template <int NT, bool kTall, bool kWhole>
-__global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const LinearFewParams p) {
-  constexpr int kRows = kTall ? 32 : 8;
-  constexpr int kSpan = kTall ? 64 : 256;  // k of a warp's step
-  constexpr int kBlocks = kTall ? 2 : 1;
-  extern __shared__ __align__(16) uint8_t few_smem[];
-  float4* red = reinterpret_cast<float4*>(few_smem);  // [warp][token tile][block][lane]
+struct LinearTile {
+  int row0, rows;  // rows 0: no tile
+  int t0, n;       // rows of x
+};
+
+__device__ __forceinline__ LinearTile linear_tile(const LinearFewParams& p, int per, int i) {
+  LinearTile t;
+  const int c = i % p.tiles, gr = i / p.tiles;
+  t.row0 = static_cast<int>(static_cast<int64_t>(p.N) * c / p.tiles);
+  t.rows = gr < p.groups ? static_cast<int>(static_cast<int64_t>(p.N) * (c + 1) / p.tiles) - t.row0 : 0;
+  t.t0 = gr * per;
+  t.n = min(per, p.M - t.t0);
+  return t;
+}
+
+template <int NT, int kSpan, int kDepth, bool kWhole>
+__global__ void __launch_bounds__(kFewThreads, 1) linear_few_kernel(const LinearFewParams p) {
+  constexpr int kWide = 64 * kSpan;               // k of a warp's step
+  constexpr int kBlocks = kSpan == 1 ? 2 : 1;     // blocks of 16 rows (kSpan 4: 8 rows)
+  __shared__ float4 red[2][kFewWarps][kBlocks][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  const int row0 = static_cast<int>(static_cast<int64_t>(p.N) * blockIdx.x / gridDim.x);
-  const int row1 = static_cast<int>(static_cast<int64_t>(p.N) * (blockIdx.x + 1) / gridDim.x);
-  const int steps = (p.K + kFewWarps * kSpan - 1) / (kFewWarps * kSpan);
-  const int nt = (p.M + 7) >> 3;
+  const int rounds = (p.K + kFewWarps * kWide * kDepth - 1) / (kFewWarps * kWide * kDepth);
+  // a weight that several groups read stays in L2
+  const uint64_t policy = p.groups > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing here waits on a barrier in memory
 
-  const __nv_bfloat16* xr[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-    xr[j] = j * 8 + g < p.M ? p.x + static_cast<int64_t>(j * 8 + g) * p.ldx : nullptr;
-
-  const uint64_t policy = l2_policy_evict_first();
-  auto load = [&](FewA& a, int rb, int step) {
-    const int k0 = (step * kFewWarps + warp) * kSpan + q * 16;
+  FewA aw[kDepth];
+  uint4 bx[kDepth][2 * kSpan];
+  // where piece (m, half) of a step lies: its row (kSpan 1: four rows 8 apart, 2: two
+  // rows, 4: one) and its chunk of k
+  auto load = [&](FewA& a, uint4 (&b)[2 * kSpan], const LinearTile& t, int step) {
+    const int k0 = (step * kFewWarps + warp) * kWide + q * 16;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int row = rb + g + (kTall ? 16 * m + 8 * half : 0);
-        const int k = k0 + (kTall ? 0 : 64 * (2 * m + half));
-        linear_ldw<kWhole>(a.v[m][half], p.w + static_cast<int64_t>(row) * p.ldw, k, p.K, row < row1,
-                           policy);
+        const int row = g + (kSpan == 1 ? 16 * m + 8 * half : kSpan == 2 ? 8 * half : 0);
+        const int k = k0 + 64 * (kSpan == 1 ? 0 : kSpan == 2 ? m : 2 * m + half);
+        linear_ldw<kWhole>(a.v[m][half], p.w + static_cast<int64_t>(t.row0 + row) * p.ldw, k, p.K,
+                           row < t.rows, policy);
       }
+#pragma unroll
+    for (int i = 0; i < 2 * kSpan; ++i) {
+      const int k = k0 + 64 * (i >> 1) + 8 * (i & 1);
+      b[i] = few_ldx(p.x + static_cast<int64_t>(t.t0 + g) * p.ldx + k, t.rows > 0 && g < t.n && k < p.K);
+    }
   };
 
-  FewA a0, a1;
-  load(a0, row0, 0);
-  for (int rb = row0; rb < row1; rb += kRows) {
-    float acc[2][NT][4];
+  int tile = blockIdx.x;
+  LinearTile cur = linear_tile(p, NT * 8, tile);
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+  for (int d = 0; d < kDepth; ++d) load(aw[d], bx[d], cur, d);
+  int flip = 0;
+  while (cur.rows > 0) {
+    tile += gridDim.x;
+    const LinearTile next = linear_tile(p, NT * 8, tile);
+    float acc[NT][2][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-    for (int step = 0; step < steps; ++step) {
-      const bool last = step + 1 == steps;
-      load(a1, last ? rb + kRows : rb, last ? 0 : step + 1);
-      const int kofs = (step * kFewWarps + warp) * kSpan + q * 16;
-      if constexpr (kTall) {
-        few_mul<NT>(acc, a0, xr, nt, kofs, p.K);
-      } else {
-        // the four chunks lie behind one another in k; rows 8..15 of the MMA are empty
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          if (j < nt) {
+        for (int i = 0; i < 4; ++i) acc[j][m][i] = 0.0f;
+    for (int round = 0; round < rounds; ++round) {
+      const bool last = round + 1 == rounds;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+      for (int d = 0; d < kDepth; ++d) {
+        const int step = round * kDepth + d;
+        const int k0 = (step * kFewWarps + warp) * kWide;
+        if (k0 < p.K) {
 #pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                const int k = kofs + 64 * i + 8 * s;
-                const uint4 b = few_ldx(xr[j] + k, xr[j] != nullptr && k < p.K);
-                const uint32_t* lo = a0.v[i >> 1][i & 1].r + 4 * s;
-                few_mma(acc[0][j], lo[0], 0u, lo[1], 0u, b.x, b.y);
-                few_mma(acc[0][j], lo[2], 0u, lo[3], 0u, b.z, b.w);
+          for (int j = 0; j < NT; ++j)
+            if (j * 8 < cur.n) {
+              const __nv_bfloat16* xr = p.x + static_cast<int64_t>(cur.t0 + j * 8 + g) * p.ldx;
+#pragma unroll
+              for (int i = 0; i < 2 * kSpan; ++i) {
+                const int z = i >> 1, s = i & 1;
+                const int k = k0 + q * 16 + 64 * z + 8 * s;
+                const uint4 b = j == 0 ? bx[d][i] : few_ldx(xr + k, j * 8 + g < cur.n && k < p.K);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                  if (kSpan == 2 && m != z) continue;
+                  if (kSpan == 4 && m != (z >> 1)) continue;
+                  const uint32_t* lo = aw[d].v[m][kSpan == 4 ? z & 1 : 0].r + 4 * s;
+                  const uint32_t* hi = aw[d].v[m][1].r + 4 * s;
+                  few_mma(acc[j][m], lo[0], kSpan == 4 ? 0u : hi[0], lo[1], kSpan == 4 ? 0u : hi[1], b.x,
+                          b.y);
+                  few_mma(acc[j][m], lo[2], kSpan == 4 ? 0u : hi[2], lo[3], kSpan == 4 ? 0u : hi[3], b.z,
+                          b.w);
+                }
               }
-          }
+            }
+        }
+        if (last)
+          load(aw[d], bx[d], next, d);
+        else
+          load(aw[d], bx[d], cur, step + kDepth);
       }
-      a0 = a1;
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      if (j < nt)
+      if (j * 8 < cur.n) {
+        float4(*buf)[kBlocks][32] = red[flip];
+        flip ^= 1;
+        if (kSpan == 1) {
+          buf[warp][0][lane] = make_float4(acc[j][0][0], acc[j][0][1], acc[j][0][2], acc[j][0][3]);
+          buf[warp][kBlocks - 1][lane] = make_float4(acc[j][1][0], acc[j][1][1], acc[j][1][2], acc[j][1][3]);
+        } else {
+          buf[warp][0][lane] = make_float4(acc[j][0][0] + acc[j][1][0], acc[j][0][1] + acc[j][1][1],
+                                           acc[j][0][2] + acc[j][1][2], acc[j][0][3] + acc[j][1][3]);
+        }
+        __syncthreads();
+        // thread i: output row i % (16 kBlocks) (neighbours write neighbouring
+        // outputs), token i / (16 kBlocks); in a block, (row, token) is lane
+        // 4 (row % 8) + token / 2, register 2 (row / 8) + token % 2
+        const float* rf = reinterpret_cast<const float*>(&buf[0][0][0]);
+        const int i = threadIdx.x;
+        const int row = i % (16 * kBlocks), col = i / (16 * kBlocks);
+        if (col < 8 && row < cur.rows && j * 8 + col < cur.n) {
+          const int at = (row >> 4) * 128 + ((row & 7) * 4 + (col >> 1)) * 4 + ((row >> 3) & 1) * 2 + (col & 1);
+          float s = 0.0f;
 #pragma unroll
-        for (int m = 0; m < kBlocks; ++m)
-          red[((warp * NT + j) * kBlocks + m) * 32 + lane] =
-              make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
-    __syncthreads();
-    // value (lane l, register v) of a block: row l/4 + 8*(v/2), token 2*(l%4) + v%2
-    const float* rf = reinterpret_cast<const float*>(red);
-    for (int i = threadIdx.x; i < nt * kBlocks * 128; i += kFewThreads) {
-      const int j = i / (kBlocks * 128), m = (i >> 7) % kBlocks, l = (i >> 2) & 31, v = i & 3;
-      const int row = rb + 16 * m + (l >> 2) + 8 * (v >> 1);
-      const int col = j * 8 + 2 * (l & 3) + (v & 1);
-      if ((kTall || v < 2) && row < row1 && col < p.M) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) s += rf[((w * NT + j) * kBlocks + m) * 128 + (i & 127)];
-        linear_store(p.e, col, row, s);
+          for (int w = 0; w < kFewWarps; ++w) s += rf[w * kBlocks * 128 + at];
+          linear_store(p.e, cur.t0 + j * 8 + col, cur.row0 + row, s);
+        }
       }
-    }
-    __syncthreads();
+    cur = next;
   }
 }
 
-template <int NT, bool kTall, bool kWhole>
+template <int NT, int kSpan, int kDepth>
 cudaError_t run(const LinearFewParams& p, int grid, cudaStream_t stream) {
-  const int smem = kFewWarps * NT * (kTall ? 2 : 1) * 32 * static_cast<int>(sizeof(float4));
-  static bool set[64] = {};  // the attribute holds for the process: once per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!set[dev]) {
-    e = cudaFuncSetAttribute(linear_few_kernel<NT, kTall, kWhole>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    set[dev] = true;
-  }
-  linear_few_kernel<NT, kTall, kWhole><<<grid, kFewThreads, smem, stream>>>(p);
+  const bool whole = p.K % 16 == 0 && p.ldw % 16 == 0 && (reinterpret_cast<uintptr_t>(p.w) & 31u) == 0;
+  if (whole)
+    linear_few_kernel<NT, kSpan, kDepth, true><<<grid, kFewThreads, 0, stream>>>(p);
+  else
+    linear_few_kernel<NT, kSpan, kDepth, false><<<grid, kFewThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int NT>
-cudaError_t run_few(const LinearFewParams& p, cudaStream_t stream) {
-  const int most = 2 * device_sm_count();
-  const int grid = p.N < most ? p.N : most;
-  const bool tall = p.N > 8 * grid;
-  const bool whole = p.K % 16 == 0 && p.ldw % 16 == 0 && (reinterpret_cast<uintptr_t>(p.w) & 31u) == 0;
-  if (tall)
-    return whole ? run<NT, true, true>(p, grid, stream) : run<NT, true, false>(p, grid, stream);
-  return whole ? run<NT, false, true>(p, grid, stream) : run<NT, false, false>(p, grid, stream);
+cudaError_t run_few(LinearFewParams p, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  p.groups = (p.M + NT * 8 - 1) / (NT * 8);
+  // as many tiles a CTA as tiles of at most 32 rows need, and then rows that make
+  // these tiles equal
+  const long long rows_all = static_cast<long long>(p.N) * p.groups;
+  const long long turns = (rows_all + 32ll * sms - 1) / (32ll * sms);
+  long long rows = (rows_all + sms * turns - 1) / (sms * turns);
+  if (rows > 32) rows = 32;
+  p.tiles = static_cast<int>((p.N + rows - 1) / rows);
+  const long long all = static_cast<long long>(p.tiles) * p.groups;
+  const int grid = static_cast<int>(all < sms ? all : sms);
+  const int most = (p.N + p.tiles - 1) / p.tiles;
+  if (most <= 8) return run<NT, 4, NT == 4 ? 2 : 3>(p, grid, stream);
+  if (most <= 16) return run<NT, 2, NT == 4 ? 3 : 4>(p, grid, stream);
+  return run<NT, 1, NT == 4 ? 3 : 4>(p, grid, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_few(const LinearLaunch& L, cudaStream_t stream) {
-  LinearFewParams p;
+  LinearFewParams p = {};
   p.M = L.M;
   p.N = L.N;
   p.K = L.K;
@@ -193,8 +230,7 @@ cudaError_t launch_linear_few(const LinearLaunch& L, cudaStream_t stream) {
   p.status = L.status;
   if (p.M <= 8) return run_few<1>(p, stream);
   if (p.M <= 16) return run_few<2>(p, stream);
-  if (p.M <= 32) return run_few<4>(p, stream);
-  return run_few<8>(p, stream);
+  return run_few<4>(p, stream);
 }
 
 }  // namespace moe
