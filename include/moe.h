@@ -491,7 +491,7 @@ moe_status moe_experts_forward_few(const moe_problem* prob, const void* hidden, 
  * 64 rows run in a kernel that streams the weight, more on tcgen05 tiles.
  * Errors: MOE_ERR_INVALID_ARG for null, misaligned or negative arguments, a pitch
  * below its row, a bad act; MOE_ERR_UNSUPPORTED for K % 8, ldx % 8 or ldw % 8 and
- * for sizes above 2^24; MOE_ERR_WORKSPACE. `workspace` (16-byte aligned) holds the
+ * for sizes above 2^24; MOE_ERR_WORKSPACE. `workspace` (32-byte aligned) holds the
  * device status word (its first int32, zeroed by the call; MOE_DEV_TIMEOUT) and
  * partial sums; calls whose work may overlap need one each.
  * moe_linear_workspace_bytes returns 0 for a descriptor that moe_linear refuses. */

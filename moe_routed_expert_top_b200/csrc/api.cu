@@ -225,23 +225,58 @@ moe_status check_linear(const moe_linear_desc* d, LinearShape* out) {
 
 int64_t linear_forward_bytes(const LinearShape& d) {
   if (d.M <= moe::kLinearFewRows) return 1024;
-  return 1024 + 4 * moe::linear_gemm_partial(d.M, d.N, d.K, d.y_f32);
+  if (d.N == 0) return 1024;
+  moe::LinearProduct g;
+  g.M = d.M;
+  g.N = d.N;
+  g.K = d.K;
+  g.e.y_f32 = d.y_f32;
+  return 1024 + 4 * moe::linear_gemm_partial(&g, 1);
 }
 
 struct LinearBackwardPlan {
   int64_t dz = 0, lines = 0, partial = 0, total = 0;
 };
 
+// The backward pass's products, sizes and operand orders: which 1 dx, 2 dw, 3 both.
+// Returns their number.
+int linear_backward_products(const LinearShape& d, int which, moe::LinearProduct* g) {
+  int count = 0;
+  if (which & 1) {
+    moe::LinearProduct& q = g[count++];
+    q.M = d.M;
+    q.N = d.K;
+    q.K = d.N;
+    q.b_mn = 1;
+  }
+  if (which & 2) {
+    moe::LinearProduct& q = g[count++];
+    q.M = d.N;
+    q.N = d.K;
+    q.K = d.M;
+    q.a_mn = 1;
+    q.b_mn = 1;
+  }
+  return count;
+}
+
 LinearBackwardPlan plan_linear_backward(const LinearShape& d) {
   LinearBackwardPlan b;
   b.dz = 1024;  // after the status word
+  if (d.M == 0 || d.N == 0) {
+    b.total = 1024;
+    return b;
+  }
   b.lines = round_up(b.dz + static_cast<int64_t>(d.M) * round_up(d.N, 8) * 2, 1024);
-  b.partial = round_up(
-      b.lines + static_cast<int64_t>(moe::linear_dz_lines(d.M)) * d.N * 4, 1024);
-  // dx and dw follow one another on the stream and share the partial sums' room
-  const int64_t px = d.N > 0 ? moe::linear_gemm_partial(d.M, d.K, d.N, 0) : 0;
-  const int64_t pw = d.M > 0 ? moe::linear_gemm_partial(d.N, d.K, d.M, 0) : 0;
-  b.total = round_up(b.partial + 4 * (px > pw ? px : pw), 1024);
+  b.partial = round_up(b.lines + static_cast<int64_t>(moe::linear_dz_lines(d.M, d.N)) * d.N * 4, 1024);
+  int64_t most = 0;  // whichever gradients the call asks for
+  for (int which = 1; which <= 3; ++which) {
+    moe::LinearProduct g[2];
+    const int count = linear_backward_products(d, which, g);
+    const int64_t n = moe::linear_gemm_partial(g, count);
+    if (n > most) most = n;
+  }
+  b.total = round_up(b.partial + 4 * most, 1024);
   return b;
 }
 
@@ -981,14 +1016,14 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
   if (d.M == 0 || d.N == 0) return MOE_OK;
   if (x == nullptr || w == nullptr || y == nullptr || workspace == nullptr)
     return MOE_ERR_INVALID_ARG;
-  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(workspace, 16) ||
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(workspace, 32) ||
       !aligned(bias, desc->bias_f32 ? 4 : 2) || !aligned(residual, desc->res_f32 ? 4 : 2) ||
       !aligned(y, desc->y_f32 ? 4 : 2) || !aligned(z, 2))
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < static_cast<size_t>(linear_forward_bytes(d))) return MOE_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  moe::LinearLaunch g;
+  moe::LinearProduct g;
   g.M = d.M;
   g.N = d.N;
   g.K = d.K;
@@ -1007,14 +1042,12 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
   g.e.ldr = d.ldr;
   g.e.ldy = d.ldy;
   g.e.ldz = d.ldz;
-  g.partial = reinterpret_cast<float*>(base + 1024);
-  g.status = reinterpret_cast<int32_t*>(base);
+  int32_t* status = reinterpret_cast<int32_t*>(base);
   if (d.M <= moe::kLinearFewRows) {
-    MOE_CUDA_TRY(moe::launch_linear_few(g, st));
+    MOE_CUDA_TRY(moe::launch_linear_few(g, status, st));
     return MOE_OK;
   }
-  MOE_CUDA_TRY(cudaMemsetAsync(base, 0, sizeof(int32_t), st));
-  MOE_CUDA_TRY(moe::launch_linear_gemm(g, st));
+  MOE_CUDA_TRY(moe::launch_linear_gemm(&g, 1, reinterpret_cast<float*>(base + 1024), status, st));
   return MOE_OK;
 }
 
@@ -1032,7 +1065,7 @@ moe_status moe_linear_backward(const moe_linear_desc* desc, const void* dy, cons
   if (s != MOE_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (!aligned(dy, desc->y_f32 ? 4 : 2) || !aligned(x, 16) || !aligned(w, 16) || !aligned(z, 2) ||
-      !aligned(dx, 16) || !aligned(dw, 16) || !aligned(dbias, 4) || !aligned(workspace, 16))
+      !aligned(dx, 16) || !aligned(dw, 16) || !aligned(dbias, 4) || !aligned(workspace, 32))
     return MOE_ERR_INVALID_ARG;
   if (d.M == 0) {  // sums over no rows
     if (dw != nullptr && d.N > 0)
@@ -1053,7 +1086,6 @@ moe_status moe_linear_backward(const moe_linear_desc* desc, const void* dy, cons
   const LinearBackwardPlan b = plan_linear_backward(d);
   if (ws_bytes < static_cast<size_t>(b.total)) return MOE_ERR_WORKSPACE;
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  MOE_CUDA_TRY(cudaMemsetAsync(base, 0, sizeof(int32_t), st));
   // the products take dy itself where it is already their operand
   const bool direct = desc->act == MOE_ACT_NONE && !desc->y_f32 && d.ldy % 8 == 0 && aligned(dy, 16);
   const bool products = dx != nullptr || dw != nullptr;
@@ -1081,37 +1113,23 @@ moe_status moe_linear_backward(const moe_linear_desc* desc, const void* dy, cons
     }
     MOE_CUDA_TRY(moe::launch_linear_dz(e, st));
   }
-  moe::LinearLaunch g;
-  g.partial = reinterpret_cast<float*>(base + b.partial);
-  g.status = reinterpret_cast<int32_t*>(base);
-  if (dx != nullptr) {
-    g.M = d.M;
-    g.N = d.K;
-    g.K = d.N;
-    g.a_mn = 0;
-    g.b_mn = 1;
-    g.A = dz;
-    g.lda = lddz;
-    g.B = w;
-    g.ldb = d.ldw;
-    g.e.y = dx;
-    g.e.ldy = d.K;
-    MOE_CUDA_TRY(moe::launch_linear_gemm(g, st));
+  moe::LinearProduct g[2];
+  const int count = linear_backward_products(d, (dx != nullptr ? 1 : 0) | (dw != nullptr ? 2 : 0), g);
+  for (int i = 0; i < count; ++i) {
+    const bool first = i == 0 && dx != nullptr;
+    g[i].A = dz;
+    g[i].lda = lddz;
+    g[i].B = first ? w : x;
+    g[i].ldb = first ? d.ldw : d.ldx;
+    g[i].e.y = first ? dx : dw;
+    g[i].e.ldy = d.K;
   }
-  if (dw != nullptr) {
-    g.M = d.N;
-    g.N = d.K;
-    g.K = d.M;
-    g.a_mn = 1;
-    g.b_mn = 1;
-    g.A = dz;
-    g.lda = lddz;
-    g.B = x;
-    g.ldb = d.ldx;
-    g.e.y = dw;
-    g.e.ldy = d.K;
-    MOE_CUDA_TRY(moe::launch_linear_gemm(g, st));
+  if (count == 0) {  // dbias alone waits on nothing
+    MOE_CUDA_TRY(cudaMemsetAsync(base, 0, sizeof(int32_t), st));
+    return MOE_OK;
   }
+  MOE_CUDA_TRY(moe::launch_linear_gemm(g, count, reinterpret_cast<float*>(base + b.partial),
+                                       reinterpret_cast<int32_t*>(base), st));
   return MOE_OK;
 }
 

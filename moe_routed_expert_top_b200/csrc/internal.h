@@ -201,22 +201,24 @@ struct LinearEpilogue {
 };
 // C[m, n] = epilogue(sum_k A(m, k) B(n, k)), A and B bf16. a_mn: A is stored
 // [K][M] (row k holds the M values of that k), else [M][K]; b_mn likewise.
-struct LinearLaunch {
+struct LinearProduct {
   int M = 0, N = 0, K = 0;
   int a_mn = 0, b_mn = 0;
   const void* A = nullptr;
   const void* B = nullptr;
   long long lda = 0, ldb = 0;  // row pitches, elements
   LinearEpilogue e;
-  float* partial = nullptr;    // linear_gemm_partial() floats
-  int32_t* status = nullptr;
 };
+// Rows of x up to which the weight-streaming kernel runs instead of the tiles.
 constexpr int kLinearFewRows = 64;
-cudaError_t launch_linear_few(const LinearLaunch& L, cudaStream_t stream);
-cudaError_t launch_linear_gemm(const LinearLaunch& L, cudaStream_t stream);
-long long linear_gemm_partial(int M, int N, int K, int y_f32);
+cudaError_t launch_linear_few(const LinearProduct& L, int32_t* status, cudaStream_t stream);
+// One or two products in one launch (count 1 or 2); partial: linear_gemm_partial()
+// floats (which goes by the products' sizes and y_f32), 32-byte aligned.
+cudaError_t launch_linear_gemm(const LinearProduct* L, int count, float* partial, int32_t* status,
+                               cudaStream_t stream);
+long long linear_gemm_partial(const LinearProduct* L, int count);
 // dz bf16 [M, ldz_out] = dy * act'(z) (null: only the column sums); the sums of
-// dz's columns before rounding go to dbias through `lines` [linear_dz_lines(M)][N].
+// dz's columns before rounding go to dbias through `lines` [linear_dz_lines(M, N)][N].
 struct LinearDzLaunch {
   int M = 0, N = 0, act = kActNone, dy_f32 = 0;
   const void* dy = nullptr;
@@ -227,7 +229,7 @@ struct LinearDzLaunch {
   float* dbias = nullptr;
 };
 cudaError_t launch_linear_dz(const LinearDzLaunch& L, cudaStream_t stream);
-int linear_dz_lines(int M);
+int linear_dz_lines(int M, int N);
 // out[i][c] = sum over lines l (in order) of table[i][l][c], i < tables.
 cudaError_t launch_sum_lines(const float* table, int tables, int lines, int H, float* out0,
                              float* out1, cudaStream_t stream);

@@ -11,24 +11,27 @@
 // either, by a bit of its instruction descriptor and another reading of the
 // shared-memory tile, so no operand is transposed in memory.
 //
-// What bounds it: the tensor cores at training sizes. A CTA pair (cluster of two
-// on one TPC) computes a 256 x BN tile with 256-row MMAs (cta_group::2): each CTA
-// fetches its 128 rows of A and its half of B's rows, 16 KB + BN/2*128 B per 64
-// of k against the 16 KB + BN*128 B that a tile of its own would take. Two
-// accumulators in tensor memory let a tile's epilogue run under the next one's
-// main loop. Few tiles (a narrow output, few rows): the k range is split over
-// the idle pairs, each part leaves fp32 sums in the workspace and a second kernel
-// adds them in order and applies the epilogue. An fp32 result is always made of
-// parts of at most 2048 k: the tensor core's fp32 accumulator drops the low bits
-// of each product sum it adds (about 1e-5 of the result at k = 7168, measured),
-// and adding parts in full fp32 keeps an fp32 result near 4e-6.
+// What bounds it: at training sizes the operands' way from L2 to the SMs, close
+// behind it the tensor cores. A CTA pair (cluster of two on one TPC) computes a
+// 256 x 256 tile with 256-row MMAs (cta_group::2): each CTA fetches its 128 rows of A
+// and its half of B's rows, 64 KB a stage of 128 k against the 96 KB that a tile of
+// its own would take; the chip reads about 9.4 TB/s this way (measured at 8192^3).
+// Two accumulators in tensor memory let a tile's epilogue run under the next
+// one's main loop. Few tiles (a narrow output, few rows): k is split over the idle
+// pairs, each part leaves fp32 sums in the workspace and a second kernel adds them
+// in order and applies the epilogue. An fp32 result is always made of parts of at
+// most 2048 k: the tensor core's fp32 accumulator drops the low bits of each
+// product sum it adds (about 1e-5 of the result at k = 7168, measured), and adding
+// parts in full fp32 keeps an fp32 result below 1e-6.
 //
 // Operand tiles in shared memory (128-byte swizzle, written by TMA):
-//   k contiguous   rows of 64 k = 128 bytes, 8-row groups 1024 B apart; a K = 16
-//                  step is 32 bytes along the row;
-//   MN contiguous  boxes of 64 output indices (128 bytes) x 64 k rows = 8 KB: 8-k
-//                  groups 1024 B apart (stride offset), the next 64 indices 8 KB
-//                  on (leading offset); a K = 16 step is two groups, 2 KB.
+//   k contiguous   two blocks of 64 k; a block has a 128-byte row for each output
+//                  index, 8-row groups 1024 B apart; a K = 16 step is 32 bytes along
+//                  the row;
+//   MN contiguous  a block for each 64 output indices; a block has a 128-byte row for
+//                  each of the 128 k: 8-k groups 1024 B apart (stride offset), the
+//                  next 64 indices 16 KB on (leading offset); a K = 16 step is two
+//                  groups, 2 KB.
 // Rows and columns past the operands' ends are filled with zeros by TMA and
 // masked at the store. Every wait is bounded and sets MOE_DEV_TIMEOUT on expiry.
 #include <cuda.h>
@@ -48,55 +51,105 @@ namespace moe {
 namespace {
 
 constexpr int kLinThreads = 320;  // TMA, MMA, two groups of 4 epilogue warps
+constexpr int kMaxBn = 256;
+constexpr int kBk = 128;                         // k of a stage
+constexpr int kStages = 3;
+constexpr int kStageA = 128 * kBk * 2;           // this CTA's 128 rows of A
+constexpr int kStageB = (kMaxBn / 2) * kBk * 2;  // its half of B's rows
+constexpr int kNumAcc = 2;
+// each epilogue warp's 32 x 16 block (its rows 17 apart) and 128 bias values
+constexpr int kBlockFloats = 32 * 17 + 128;
+constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 1;
+constexpr int kLinSmem = 1024 + kStages * (kStageA + kStageB) + 8 * kBlockFloats * 4 + kNumBars * 8 + 32;
+static_assert(kLinSmem <= 227 * 1024, "shared memory");
 
-struct LinParams {
-  int M, N, K;
-  int tiles_m, tiles_n, splits;
-  int kb_total, kb_split;  // 64-wide k blocks: all, and of one split
-  float* partial;          // [splits][M][N] when splits > 1
-  int32_t* status;
-  int wide;                // every row of y, z, residual (and partial) takes 32-byte accesses
+// One product: C[m,n] = epilogue(sum_k A(m,k) B(n,k)).
+struct LinProblem {
+  int M, N;
+  int a_mn, b_mn;
+  int a_3d, b_3d;          // the operand's stage is one copy (3-D tensor map)
+  int bn;                  // tile width: a multiple of 32, at most kMaxBn
+  int tiles_m, tiles_n;
+  int splits;              // parts of each tile, along k
+  int kb_total, kb_split;  // k blocks of 128: all, and of one part
+  float* partial;          // [splits][tiles][256][bn] sums of the parts
+  int wide;                // every row of y, z and residual takes 32-byte accesses
   LinearEpilogue e;
 };
+struct LinParams {
+  LinProblem p[2];
+  int end[2];  // work items up to the end of each product
+  int32_t* status;
+};
 
-template <int BN>
-struct LCfg {
-  static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_BYTES = (BN / 2) * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 5 : 7;
-  static constexpr int NUM_ACC = 2;
-  static constexpr int TMEM_COLS = 2 * BN;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * NUM_ACC + 1;
-  // each epilogue warp's 32 x 32 block, its rows 33 apart
-  static constexpr int BLOCK_BYTES = 32 * 33 * 4;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 8 * BLOCK_BYTES + NUM_BARS * 8 + 32;
-  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+// A work item: which product, tile and k blocks.
+struct LinItem {
+  int which, tm, tn;
+  int kb0, kb1;
+  float* partial;  // of a part: its tile's [256][bn]; null: a whole tile
 };
 
 // Descriptor of an operand tile whose output index is contiguous (see above).
 __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t smem_addr) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(8192 >> 4) << 16;  // to the next 64 output indices
+  d |= static_cast<uint64_t>((kBk * 128) >> 4) << 16;  // to the next 64 output indices
   d |= static_cast<uint64_t>(1024 >> 4) << 32;  // to the next 8 k
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
 
-// Work item -> tile. Tiles go in bands of 8 along M, so that the tiles that run
-// together share operands in both directions (8 x 9 of them on 74 pairs read 17
-// operand strips instead of 75).
-__device__ __forceinline__ void lin_decode(const LinParams& p, int t, int& tm, int& tn, int& sp) {
-  const int tiles = p.tiles_m * p.tiles_n;
-  sp = t / tiles;
-  const int i = t - sp * tiles;
-  const int band = i / (8 * p.tiles_n);
+// Tiles go in bands of 8 along M, so that the tiles that run together share
+// operands in both directions (8 x 9 of them on 74 pairs read 17 operand strips
+// instead of 75).
+__device__ __forceinline__ void lin_tile(const LinProblem& p, int tile, int& tm, int& tn) {
+  const int band = tile / (8 * p.tiles_n);
   const int h = min(8, p.tiles_m - 8 * band);
-  const int r = i - band * 8 * p.tiles_n;
+  const int r = tile - band * 8 * p.tiles_n;
   tn = r / h;
   tm = 8 * band + (r - tn * h);
+}
+
+__device__ __forceinline__ LinItem lin_item(const LinParams& a, int t) {
+  LinItem it;
+  it.which = t < a.end[0] ? 0 : 1;
+  const LinProblem& p = a.p[it.which];
+  const int u = it.which ? t - a.end[0] : t;
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int part = u / tiles, tile = u - part * tiles;
+  lin_tile(p, tile, it.tm, it.tn);
+  it.kb0 = part * p.kb_split;
+  it.kb1 = min(p.kb_total, it.kb0 + p.kb_split);
+  it.partial = p.splits == 1 ? nullptr : p.partial + static_cast<long long>(u) * (256 * p.bn);
+  return it;
+}
+
+// 3-D tiled load (x = 0) completing on a barrier that may live in the pair's leader.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t smem_dst, const void* tmap, int32_t y, int32_t z,
+                                                 uint32_t bar_cluster, uint64_t cache_hint) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(y), "r"(z), "r"(bar_cluster), "l"(cache_hint)
+      : "memory");
+}
+
+// One operand's part of a stage: `rows` output indices from o0 on x 128 k from k0 on.
+__device__ __forceinline__ void lin_load(uint32_t dst, const CUtensorMap* tm, bool mn, bool three, int o0, int rows,
+                                         int k0, uint32_t bar, uint64_t pol) {
+  if (three) {
+    if (mn)
+      tma_load_3d_pair(dst, tm, k0, o0 / 64, bar, pol);
+    else
+      tma_load_3d_pair(dst, tm, o0, k0 / 64, bar, pol);
+  } else if (mn) {
+    tma_load_2d_pair(dst, tm, o0, k0, bar, pol);
+    if (rows > 64) tma_load_2d_pair(dst + kBk * 128, tm, o0 + 64, k0, bar, pol);
+  } else {
+    tma_load_2d_pair(dst, tm, k0, o0, bar, pol);
+    tma_load_2d_pair(dst + rows * 128, tm, k0 + 64, o0, bar, pol);
+  }
 }
 
 __device__ __forceinline__ void lin_st8(void* p, const uint32_t* v) {
@@ -130,12 +183,10 @@ __device__ __forceinline__ void lin_act32(uint32_t (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(linear_act(__uint_as_float(v[i]), kAct));
 }
 
-// The epilogue of 32 columns n.. of row m, all accesses 32 bytes wide.
-__device__ __forceinline__ void lin_store32(const LinearEpilogue& e, long long m, int n, uint32_t (&v)[32]) {
-  if (e.bias != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + linear_bias(e, n + i));
-  }
+// The epilogue of 32 columns n.. of row m, all accesses 32 bytes wide. v: the sums
+// with their bias; res: the residual's values if they are bf16.
+__device__ __forceinline__ void lin_store32(const LinearEpilogue& e, long long m, int n, uint32_t (&v)[32],
+                                            const uint32_t (&res)[16]) {
   if (e.z != nullptr) lin_store32_bf16(static_cast<__nv_bfloat16*>(e.z) + m * e.ldz + n, v);
   if (e.act == kActRelu)
     lin_act32<kActRelu>(v);
@@ -144,26 +195,21 @@ __device__ __forceinline__ void lin_store32(const LinearEpilogue& e, long long m
   else if (e.act == kActGelu)
     lin_act32<kActGelu>(v);
   if (e.res != nullptr) {
-    uint32_t r[8];
     if (e.res_f32) {
       const float* src = static_cast<const float*>(e.res) + m * e.ldr + n;
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
+        uint32_t r[8];
         lin_ld8(r, src + i);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           v[i + j] = __float_as_uint(__uint_as_float(v[i + j]) + __uint_as_float(r[j]));
       }
     } else {
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.res) + m * e.ldr + n;
 #pragma unroll
-      for (int i = 0; i < 32; i += 16) {
-        lin_ld8(r, src + i);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[i + 2 * j] = __float_as_uint(__uint_as_float(v[i + 2 * j]) + bf16lo_to_f32(r[j]));
-          v[i + 2 * j + 1] = __float_as_uint(__uint_as_float(v[i + 2 * j + 1]) + bf16hi_to_f32(r[j]));
-        }
+      for (int i = 0; i < 16; ++i) {
+        v[2 * i] = __float_as_uint(__uint_as_float(v[2 * i]) + bf16lo_to_f32(res[i]));
+        v[2 * i + 1] = __float_as_uint(__uint_as_float(v[2 * i + 1]) + bf16hi_to_f32(res[i]));
       }
     }
   }
@@ -173,29 +219,32 @@ __device__ __forceinline__ void lin_store32(const LinearEpilogue& e, long long m
     lin_store32_bf16(static_cast<__nv_bfloat16*>(e.y) + m * e.ldy + n, v);
 }
 
-template <bool AMN, bool BMN, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
-    linear_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
-                       const __grid_constant__ CUtensorMap tmB, const LinParams p) {
-  using Cfg = LCfg<BN>;
-  constexpr int STAGES = Cfg::STAGES;
-  constexpr int NUM_ACC = Cfg::NUM_ACC;
+// 32 bf16 residual values of row m from n on, 32 bytes wide (res_f32: not taken).
+__device__ __forceinline__ void lin_fetch_res(const LinearEpilogue& e, long long m, int n, uint32_t (&r)[16]) {
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.res) + m * e.ldr + n;
+  lin_ld8(r, src);
+  lin_ld8(r + 8, src + 16);
+}
 
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
+    linear_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
+                       const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
+                       const __grid_constant__ LinParams args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
-  uint8_t* sB = smem + STAGES * Cfg::A_BYTES;
-  float* sBlock = reinterpret_cast<float*>(sB + STAGES * Cfg::B_BYTES);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sBlock) + 8 * Cfg::BLOCK_BYTES);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
+  uint8_t* sB = smem + kStages * kStageA;
+  float* sBlock = reinterpret_cast<float*>(sB + kStages * kStageB);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sBlock + 8 * kBlockFloats);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const uint32_t full0 = smem_u32(bars);
-  const uint32_t empty0 = full0 + 8 * STAGES;
-  const uint32_t tfull0 = empty0 + 8 * STAGES;
-  const uint32_t tempty0 = tfull0 + 8 * NUM_ACC;
-  const uint32_t drain_bar = tempty0 + 8 * NUM_ACC;
+  const uint32_t empty0 = full0 + 8 * kStages;
+  const uint32_t tfull0 = empty0 + 8 * kStages;
+  const uint32_t tempty0 = tfull0 + 8 * kNumAcc;
+  const uint32_t drain_bar = tempty0 + 8 * kNumAcc;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -203,29 +252,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
+  int32_t* status = args.status;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    // (a wait gives up after seconds, long after this)
+    if (blockIdx.x == 0) *status = 0;
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
-    for (int a = 0; a < NUM_ACC; ++a) {
+    for (int a = 0; a < kNumAcc; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
       mbar_init(tempty0 + 8 * a, 16);  // 8 epilogue warps in each CTA of the pair
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     mbar_fence_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmA0);
+    tma_prefetch_desc(&tmB0);
+    if (args.end[1] > args.end[0]) {
+      tma_prefetch_desc(&tmA1);
+      tma_prefetch_desc(&tmB1);
+    }
   }
-  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), Cfg::TMEM_COLS);
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), kNumAcc * kMaxBn);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or load completion
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int items = p.tiles_m * p.tiles_n * p.splits;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
@@ -235,37 +290,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       uint32_t phase = 0;
       uint32_t issued = 0;
       bool ok = true;
-      for (int t = pair; ok && t < items; t += npairs) {
-        int tm, tn, sp;
-        lin_decode(p, t, tm, tn, sp);
-        const int m0 = tm * 256 + static_cast<int>(rank) * 128;
-        const int n0 = tn * BN + static_cast<int>(rank) * (BN / 2);
-        const int kb1 = min(p.kb_total, (sp + 1) * p.kb_split);
-        for (int kb = sp * p.kb_split; kb < kb1; ++kb) {
-          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
+      for (int t = pair; ok && t < args.end[1]; t += npairs) {
+        const LinItem it = lin_item(args, t);
+        const LinProblem& p = args.p[it.which];
+        const CUtensorMap* tmA = it.which ? &tmA1 : &tmA0;
+        const CUtensorMap* tmB = it.which ? &tmB1 : &tmB0;
+        const int half = p.bn / 2;
+        const int m0 = it.tm * 256 + static_cast<int>(rank) * 128;
+        const int n0 = it.tn * p.bn + static_cast<int>(rank) * half;
+        const uint32_t bytes = kStageA + (p.b_mn ? (half + 63) / 64 * kBk * 128 : half * kBk * 2);
+        const bool a_mn = p.a_mn, b_mn = p.b_mn, a_3d = p.a_3d, b_3d = p.b_3d;
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, status)) {
             ok = false;
             break;
           }
           const uint32_t fb_local = full0 + 8 * stage;
           const uint32_t fb = cluster_map_shared(fb_local, 0);
-          if (leader) mbar_arrive_expect_tx(fb_local, 2u * Cfg::STAGE_BYTES);
-          const uint32_t a_dst = smem_u32(sA + stage * Cfg::A_BYTES);
-          const uint32_t b_dst = smem_u32(sB + stage * Cfg::B_BYTES);
-          if constexpr (AMN) {
-            tma_load_2d_pair(a_dst, &tmA, m0, kb * 64, fb, pol);
-            tma_load_2d_pair(a_dst + 8192, &tmA, m0 + 64, kb * 64, fb, pol);
-          } else {
-            tma_load_2d_pair(a_dst, &tmA, kb * 64, m0, fb, pol);
-          }
-          if constexpr (BMN) {
-#pragma unroll
-            for (int i = 0; i < BN / 128; ++i)
-              tma_load_2d_pair(b_dst + 8192 * i, &tmB, n0 + 64 * i, kb * 64, fb, pol);
-          } else {
-            tma_load_2d_pair(b_dst, &tmB, kb * 64, n0, fb, pol);
-          }
+          if (leader) mbar_arrive_expect_tx(fb_local, 2u * bytes);
+          const uint32_t a_dst = smem_u32(sA + stage * kStageA);
+          const uint32_t b_dst = smem_u32(sB + stage * kStageB);
+          lin_load(a_dst, tmA, a_mn, a_3d, m0, 128, kb * kBk, fb, pol);
+          lin_load(b_dst, tmB, b_mn, b_3d, n0, half, kb * kBk, fb, pol);
           ++issued;
-          if (++stage == STAGES) {
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -277,22 +325,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         // both halves' bytes); the other CTA waits for the stages' release. One
         // deadline bounds the drain, the cluster barrier at the end keeps both
         // CTAs alive until both have drained.
-        const uint32_t n = issued < static_cast<uint32_t>(STAGES) ? issued : STAGES;
+        const uint32_t n = issued < static_cast<uint32_t>(kStages) ? issued : kStages;
         const uint64_t deadline = globaltimer_ns() + kWaitLimitNs;
         int s = stage;
         uint32_t ph = phase;
         for (uint32_t i = 0; i < n; ++i) {
           if (--s < 0) {
-            s = STAGES - 1;
+            s = kStages - 1;
             ph ^= 1u;
           }
           mbar_wait_until((leader ? full0 : empty0) + 8 * s, ph, deadline);
         }
       } else {
         // every load this CTA issued has been consumed (its stage released) before leaving
-        for (int i = 0; i < STAGES; ++i) {
-          mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status);
-          if (++stage == STAGES) {
+        for (int i = 0; i < kStages; ++i) {
+          mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, status);
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -302,42 +350,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader only)
     if (lane == 0 && leader) {
-      constexpr uint32_t idesc = idesc_bf16_f32(256, BN) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
-      constexpr uint64_t a_step = AMN ? 2048 >> 4 : 32 >> 4;
-      constexpr uint64_t b_step = BMN ? 2048 >> 4 : 32 >> 4;
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int t = pair; ok && t < items; t += npairs) {
-        const int sp = t / (p.tiles_m * p.tiles_n);
-        const int kbs = min(p.kb_total, (sp + 1) * p.kb_split) - sp * p.kb_split;
-        if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1u, abort_flag, p.status)) break;
+      for (int t = pair; ok && t < args.end[1]; t += npairs) {
+        const LinItem it = lin_item(args, t);
+        const LinProblem& p = args.p[it.which];
+        const int kbs = it.kb1 - it.kb0;
+        const bool a_mn = p.a_mn, b_mn = p.b_mn;
+        const uint32_t idesc =
+            idesc_bf16_f32(256, p.bn) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        // from one K = 16 step to the next, and (k contiguous) to the second 64 of k
+        const uint64_t a_step = (a_mn ? 2048 : 32) >> 4, a_half = (a_mn ? 8192 : 128 * 128) >> 4;
+        const uint64_t b_step = (b_mn ? 2048 : 32) >> 4, b_half = (b_mn ? 8192 : p.bn / 2 * 128) >> 4;
+        if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1u, abort_flag, status)) break;
         tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kMaxBn);
         for (int kb = 0; kb < kbs; ++kb) {
-          if (!mbar_wait(full0 + 8 * stage, phase, abort_flag, p.status)) {
+          if (!mbar_wait(full0 + 8 * stage, phase, abort_flag, status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_at = smem_u32(sA + stage * Cfg::A_BYTES);
-          const uint32_t b_at = smem_u32(sB + stage * Cfg::B_BYTES);
-          const uint64_t adesc = AMN ? smem_desc_mn(a_at) : smem_desc_sw128(a_at);
-          const uint64_t bdesc = BMN ? smem_desc_mn(b_at) : smem_desc_sw128(b_at);
+          const uint32_t a_at = smem_u32(sA + stage * kStageA);
+          const uint32_t b_at = smem_u32(sB + stage * kStageB);
+          const uint64_t adesc = a_mn ? smem_desc_mn(a_at) : smem_desc_sw128(a_at);
+          const uint64_t bdesc = b_mn ? smem_desc_mn(b_at) : smem_desc_sw128(b_at);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16_pair(d, adesc + a_step * k, bdesc + b_step * k, idesc, (kb | k) != 0 ? 1u : 0u);
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_pair(d, adesc + a_step * (k & 3) + a_half * (k >> 2),
+                          bdesc + b_step * (k & 3) + b_half * (k >> 2), idesc, (kb | k) != 0 ? 1u : 0u);
           mma_commit_pair_mc(empty0 + 8 * stage, 0x3);
-          if (++stage == STAGES) {
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
         mma_commit_pair_mc(tfull0 + 8 * acc, 0x3);
-        if (++acc == NUM_ACC) {
+        if (++acc == kNumAcc) {
           acc = 0;
           acc_phase ^= 1u;
         }
@@ -349,77 +402,105 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    // Group g takes the tile's columns [g BN/2, (g+1) BN/2) in runs of 32; a
-    // warp has 32 rows. Tensor memory gives a thread 32 columns of one row.
+    // A tile's columns go in runs of 32, the even ones to group 0 and the odd
+    // ones to group 1; a warp has 32 rows. Tensor memory gives a thread 32
+    // columns of one row.
     //   32-byte accesses possible: it stores them as they are (32 rows at a time,
-    //     whole sectors);
+    //     whole sectors), the residual's next run already on its way;
     //   else (odd pitches, the last columns): through shared memory, so that the
     //     lanes lie along the row (a 2-byte store to 32 rows at a time would cost
     //     more than the main loop).
     const int grp = (warp - 2) >> 2;
     const int q = warp & 3;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    float* block = sBlock + (warp - 2) * (32 * 33);
+    float* block = sBlock + (warp - 2) * kBlockFloats;
+    float* bias = block + 32 * 17;  // of the group's runs of the tile
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = pair; t < items; t += npairs) {
-      int tm, tn, sp;
-      lin_decode(p, t, tm, tn, sp);
+    for (int t = pair; t < args.end[1]; t += npairs) {
+      const LinItem it = lin_item(args, t);
+      const LinProblem& p = args.p[it.which];
+      const bool sums = it.partial != nullptr;
+      const int r0 = static_cast<int>(rank) * 128 + q * 32;  // the warp's first row of the tile
+      const long long m0 = static_cast<long long>(it.tm) * 256 + r0;
+      const int rows = static_cast<int>(min(32ll, p.M - m0));
+      const int c0 = it.tn * p.bn;
+      const int width = min(p.bn, p.N - c0);
+      const bool has_bias = !sums && p.e.bias != nullptr;
+      const bool fetch = !sums && p.wide && p.e.res != nullptr && !p.e.res_f32;
+      __syncwarp();
+      if (has_bias)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = (2 * i + grp) * 32 + lane;
+          bias[i * 32 + lane] = c < width ? linear_bias(p.e, c0 + c) : 0.0f;
+        }
+      __syncwarp();
+      uint32_t res[16];
+      if (fetch && lane < rows && grp * 32 + 32 <= width) lin_fetch_res(p.e, m0 + lane, c0 + grp * 32, res);
       bool got = true;
-      if (lane == 0) got = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.status);
+      if (lane == 0) got = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, status);
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got) break;
       tc_fence_after();
-      const long long m0 = static_cast<long long>(tm) * 256 + static_cast<int>(rank) * 128 + q * 32;
-      const int rows = static_cast<int>(min(32ll, p.M - m0));
-      const int c0 = tn * BN + grp * (BN / 2);
 #pragma unroll 1
-      for (int j = 0; j < BN / 2; j += 32) {
+      for (int j = grp * 32; j < width && rows > 0; j += 64) {
         const int n = c0 + j;
-        if (rows <= 0 || n >= p.N) break;
         uint32_t v[32];
-        tmem_ld32(lane_base + static_cast<uint32_t>(acc * BN + grp * (BN / 2) + j), v);
+        tmem_ld32(lane_base + static_cast<uint32_t>(acc * kMaxBn + j), v);
         tmem_ld_wait();
-        const int cols = min(32, p.N - n);
-        if (p.wide && cols == 32) {
-          if (lane < rows) {
-            if (p.splits > 1)
-              lin_store32_f32(p.partial + (static_cast<long long>(sp) * p.M + m0 + lane) * p.N + n, v);
-            else
-              lin_store32(p.e, m0 + lane, n, v);
+        const int cols = min(32, width - j);
+        const float* b = bias + (j >> 6) * 32;
+        if (sums) {
+          lin_store32_f32(it.partial + (r0 + lane) * p.bn + j, v);
+        } else if (p.wide && cols == 32) {
+          uint32_t now[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) now[i] = res[i];
+          if (fetch && lane < rows && j + 96 <= width) lin_fetch_res(p.e, m0 + lane, n + 64, res);
+          if (has_bias) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 bv = *reinterpret_cast<const float4*>(b + i);
+              v[i] = __float_as_uint(__uint_as_float(v[i]) + bv.x);
+              v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) + bv.y);
+              v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) + bv.z);
+              v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) + bv.w);
+            }
           }
+          if (lane < rows) lin_store32(p.e, m0 + lane, n, v, now);
         } else {
+          const int c = lane & 15;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) block[lane * 33 + i] = __uint_as_float(v[i]);
-          __syncwarp();
-          if (lane < cols) {
-            if (p.splits > 1) {
-              float* dst = p.partial + (static_cast<long long>(sp) * p.M + m0) * p.N + n + lane;
-              for (int i = 0; i < rows; ++i) dst[static_cast<long long>(i) * p.N] = block[i * 33 + lane];
-            } else {
-              const float bias = linear_bias(p.e, n + lane);
-              for (int i0 = 0; i0 < rows; i0 += 8) {
-                float res[8];
+          for (int half = 0; half < 2; ++half) {
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  res[i] = p.e.res != nullptr && i0 + i < rows ? linear_res(p.e, m0 + i0 + i, n + lane) : 0.0f;
+            for (int i = 0; i < 16; ++i) block[lane * 17 + i] = __uint_as_float(v[16 * half + i]);
+            __syncwarp();
+            if (16 * half + c < cols) {
+              const int nc = n + 16 * half + c;
+              const float bv = has_bias ? b[16 * half + c] : 0.0f;
+              for (int i0 = lane >> 4; i0 < rows; i0 += 16) {  // a half warp's rows: every second one
+                float r8[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  if (i0 + i < rows) {
+                  r8[i] = p.e.res != nullptr && i0 + 2 * i < rows ? linear_res(p.e, m0 + i0 + 2 * i, nc) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (i0 + 2 * i < rows) {
                     float z;
-                    const float y = linear_result(p.e, block[(i0 + i) * 33 + lane], bias, res[i], &z);
-                    linear_put(p.e, m0 + i0 + i, n + lane, y, z);
+                    const float y = linear_result(p.e, block[(i0 + 2 * i) * 17 + c], bv, r8[i], &z);
+                    linear_put(p.e, m0 + i0 + 2 * i, nc, y, z);
                   }
               }
             }
           }
-          __syncwarp();
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_map_shared(tempty0 + 8 * acc, 0));
-      if (++acc == NUM_ACC) {
+      if (++acc == kNumAcc) {
         acc = 0;
         acc_phase ^= 1u;
       }
@@ -431,34 +512,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+    tmem_dealloc_pair(tmem_base, kNumAcc * kMaxBn);
   }
 }
 
-// y from the splits' sums, in split order. A block has 64 columns x 4 rows.
-__global__ void __launch_bounds__(256) linear_join_kernel(const float* partial, int splits, int M, int N,
-                                                          const LinearEpilogue e) {
-  const int n = blockIdx.x * 64 + threadIdx.x;
-  if (n >= N) return;
-  const long long total = static_cast<long long>(M) * N;
-  const float bias = linear_bias(e, n);
-  for (long long m = blockIdx.y * 4 + threadIdx.y; m < M; m += gridDim.y * 4) {
-    const float* src = partial + m * N + n;
-    const float res = e.res != nullptr ? linear_res(e, m, n) : 0.0f;
-    float s = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < splits; ++k) s += src[k * total];
-    float z;
-    const float y = linear_result(e, s, bias, res, &z);
-    linear_put(e, m, n, y, z);
+// y of the tiles computed in parts: the parts' sums, in order. A block has 32 rows
+// of one tile, a thread 8 columns of 4 of them (8 loads in flight a part: with
+// one value a thread the kernel was bound by latency, 19 us against 6 for 34
+// tiles in 2 parts).
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinProblem p, int first) {
+  const int tile = first + blockIdx.y;
+  int tm, tn;
+  lin_tile(p, tile, tm, tn);
+  const int c = threadIdx.x * 8, n = tn * p.bn + c;
+  const int row0 = blockIdx.x * 32 + threadIdx.y;
+  const long long m0 = static_cast<long long>(tm) * 256 + row0;
+  if (c >= p.bn || n >= p.N || m0 >= p.M) return;
+  const long long step = static_cast<long long>(p.tiles_m) * p.tiles_n * 256 * p.bn;
+  const float* src = p.partial + (static_cast<long long>(tile) * 256 + row0) * p.bn + c;
+  float s[4][8] = {};
+  for (int k = 0; k < p.splits; ++k, src += step) {
+    float4 v[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // (rows past M were written too)
+      v[i][0] = *reinterpret_cast<const float4*>(src + i * 8 * p.bn);
+      v[i][1] = *reinterpret_cast<const float4*>(src + i * 8 * p.bn + 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        s[i][4 * j] += v[i][j].x;
+        s[i][4 * j + 1] += v[i][j].y;
+        s[i][4 * j + 2] += v[i][j].z;
+        s[i][4 * j + 3] += v[i][j].w;
+      }
+  }
+  const int cols = min(8, p.N - n);
+  float bias[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) bias[j] = j < cols ? linear_bias(p.e, n + j) : 0.0f;
+  const bool fast = p.wide && cols == 8 && !p.e.y_f32 && (p.e.res == nullptr || !p.e.res_f32);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long m = m0 + 8 * i;
+    if (m >= p.M) break;
+    if (fast) {
+      uint4 res = make_uint4(0u, 0u, 0u, 0u);
+      if (p.e.res != nullptr)
+        res = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.e.res) + m * p.e.ldr + n);
+      const uint32_t rw[4] = {res.x, res.y, res.z, res.w};
+      float y[8], z[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        y[j] = linear_result(p.e, s[i][j], bias[j], j & 1 ? bf16hi_to_f32(rw[j >> 1]) : bf16lo_to_f32(rw[j >> 1]),
+                             &z[j]);
+      if (p.e.z != nullptr)
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.e.z) + m * p.e.ldz + n) =
+            make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                       pack_bf16x2(z[6], z[7]));
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.e.y) + m * p.e.ldy + n) =
+          make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                     pack_bf16x2(y[6], y[7]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < cols) {
+          float z;
+          const float y = linear_result(p.e, s[i][j], bias[j],
+                                        p.e.res != nullptr ? linear_res(p.e, m, n + j) : 0.0f, &z);
+          linear_put(p.e, m, n + j, y, z);
+        }
+    }
   }
 }
 
 // dz = dy * act'(z), rounded to bf16 (the MMA's operand type; dbias takes the
 // unrounded values), and the column sums of a block's rows. A thread has V
 // columns, a block's 8 warps every eighth row. Bound by HBM: one pass.
-constexpr int kDzRows = 64;      // rows of a block, while kDzLines blocks cover M
-constexpr int kDzLines = 1024;
+constexpr int kDzLines = 1024;  // blocks along M, at most
 template <int V, bool kF32>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzLaunch p) {
   using Dy = typename std::conditional<kF32, float, __nv_bfloat16>::type;
@@ -543,112 +675,193 @@ bool lin_encode(CUtensorMap* map, const void* base, uint64_t inner, uint64_t row
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same as blocks of 64 inner elements: dims (64, rows, inner / 64), so that one
+// copy brings a whole stage of an operand (a copy costs its issuer about as long
+// as 8 KB take; with four copies of 8 KB a 64-wide step the backward products ran
+// at 0.85 of their speed with one of 16 KB each). Needs inner % 64 == 0: the last
+// block would otherwise read into the next row.
+bool lin_encode3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
+                 uint32_t box_blocks, uint64_t ld) {
+  auto fn = lin_encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {64, rows, inner / 64};
+  cuuint64_t strides[2] = {ld * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, box_blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand of `out` output indices and K, of which a stage takes `rows` and 128.
+bool lin_operand(CUtensorMap* map, int* three, const void* base, int mn, int out, int K, int rows, long long ld) {
+  const int inner = mn ? out : K;
+  *three = inner % 64 == 0;
+  if (*three)
+    return mn ? lin_encode3(map, base, out, K, kBk, (rows + 63) / 64, ld)
+              : lin_encode3(map, base, K, out, rows, kBk / 64, ld);
+  return mn ? lin_encode(map, base, out, K, kBk, ld) : lin_encode(map, base, K, out, rows, ld);
+}
+
+// What each product of a launch does: tile width, parts of a tile along k.
 struct LinPlan {
   int bn, tiles_m, tiles_n, splits, kb_split;
 };
 
-// Tile width and k split. 256-wide tiles move the fewest operand bytes per MMA;
-// 128-wide ones (full MMA rate too) where 256 would leave pairs idle or the
-// output is that narrow. k is split while that fills idle pairs and a part keeps
-// at least 4 blocks of 64.
-LinPlan lin_plan(int M, int N, int K, int y_f32) {
-  const int pairs = device_sm_count() / 2;
-  const int kb = (K + 63) / 64;
-  LinPlan p;
-  p.tiles_m = (M + 255) / 256;
-  p.bn = N > 128 && static_cast<long long>(p.tiles_m) * ((N + 255) / 256) * 4 >= 3ll * pairs ? 256 : 128;
-  p.tiles_n = (N + p.bn - 1) / p.bn;
-  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-  long long s = tiles > 0 ? pairs / tiles : 1;
-  if (s > kb / 4) s = kb / 4;
-  if (y_f32 && s < (kb + 31) / 32) s = (kb + 31) / 32;
-  if (s < 1) s = 1;
-  p.kb_split = static_cast<int>((kb + s - 1) / s);
-  p.splits = (kb + p.kb_split - 1) / p.kb_split;
-  return p;
+// With a tile for every pair: whole tiles of 256 x 256. (An output that leaves part
+// of the last turn idle is no slower for it: the operands' way from L2 is shared
+// by all, and cutting the last turn's tiles along k measured the same.) With
+// fewer: the tiles are cut along k into parts of g blocks that fill the pairs, or
+// are 128 wide, or both, whichever has the least modelled time in SM clocks: a
+// 128-wide k block takes about 800 + 2.4 bn, a tile 1500 that the next one does not
+// hide, and the parts' sums are written, read and added once. An fp32 result is
+// made of parts of at most 16 blocks (2048 k) throughout.
+void lin_plan(const LinearProduct* L, int count, LinPlan* out) {
+  const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
+  double best = -1.0;
+  for (int narrow = 0; narrow < 2; ++narrow) {
+    LinPlan p[2] = {};
+    int kb[2] = {0, 0}, kb_most = 0, bn = 0;
+    long long tiles = 0;
+    bool fp32 = false;
+    for (int i = 0; i < count; ++i) {
+      const int n32 = (L[i].N + 31) / 32 * 32, most = narrow ? 128 : 256;
+      p[i].bn = n32 < most ? n32 : most;
+      if (p[i].bn > bn) bn = p[i].bn;
+      p[i].tiles_m = (L[i].M + 255) / 256;
+      p[i].tiles_n = (L[i].N + p[i].bn - 1) / p[i].bn;
+      kb[i] = (L[i].K + kBk - 1) / kBk;
+      if (kb[i] > kb_most) kb_most = kb[i];
+      tiles += static_cast<long long>(p[i].tiles_m) * p[i].tiles_n;
+      if (L[i].e.y_f32 && kb[i] > 16) fp32 = true;
+    }
+    const int least = fp32 ? (kb_most + 15) / 16 : 1;
+    const int most = tiles < pairs ? least + 31 : least;
+    for (int cut = least; cut <= most; ++cut) {
+      const int g = (kb_most + cut - 1) / cut;
+      if (cut > least && g < 2) break;
+      long long items = 0;
+      double bytes = 0.0;
+      LinPlan q[2] = {p[0], p[1]};
+      for (int i = 0; i < count; ++i) {
+        q[i].splits = (kb[i] + g - 1) / g;
+        q[i].kb_split = (kb[i] + q[i].splits - 1) / q[i].splits;
+        q[i].splits = (kb[i] + q[i].kb_split - 1) / q[i].kb_split;
+        const long long n = static_cast<long long>(q[i].tiles_m) * q[i].tiles_n * q[i].splits;
+        items += n;
+        if (q[i].splits > 1) bytes += 8.0 * n * 256.0 * q[i].bn;
+      }
+      const long long turns = (items + pairs - 1) / pairs;
+      double t = static_cast<double>(turns) * (g * (800.0 + 2.4 * bn) + 1500.0);
+      if (bytes > 0.0) t += 5000.0 + bytes / 3400.0;
+      if (best < 0.0 || t < best) {
+        best = t;
+        out[0] = q[0];
+        out[1] = q[1];
+      }
+    }
+    if (!narrow && tiles >= pairs) break;
+  }
 }
 
-template <bool AMN, bool BMN, int BN>
-cudaError_t run_gemm(const LinearLaunch& L, const LinPlan& plan, cudaStream_t stream) {
-  using Cfg = LCfg<BN>;
+long long lin_partial(const LinPlan& p) {
+  return p.splits > 1 ? static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits * 256 * p.bn : 0;
+}
+
+}  // namespace
+
+long long linear_gemm_partial(const LinearProduct* L, int count) {
+  LinPlan plan[2];
+  lin_plan(L, count, plan);
+  long long n = 0;
+  for (int i = 0; i < count; ++i) n += lin_partial(plan[i]);
+  return n;
+}
+
+cudaError_t launch_linear_gemm(const LinearProduct* L, int count, float* partial, int32_t* status,
+                               cudaStream_t stream) {
   static int max_pairs_cache[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (max_pairs_cache[dev] == 0) {
-    e = cudaFuncSetAttribute(linear_gemm_kernel<AMN, BMN, BN>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    e = cudaFuncSetAttribute(linear_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() & ~1));
     cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.dynamicSmemBytes = kLinSmem;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, linear_gemm_kernel<AMN, BMN, BN>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, linear_gemm_kernel, &cfg);
     if (e != cudaSuccess) return e;
     max_pairs_cache[dev] = n > 0 ? n : 1;
   }
-  CUtensorMap tmA, tmB;
-  const bool okA = AMN ? lin_encode(&tmA, L.A, L.M, L.K, 64, L.lda) : lin_encode(&tmA, L.A, L.K, L.M, 128, L.lda);
-  const bool okB = BMN ? lin_encode(&tmB, L.B, L.N, L.K, 64, L.ldb)
-                       : lin_encode(&tmB, L.B, L.K, L.N, BN / 2, L.ldb);
-  if (!okA || !okB) return cudaErrorInvalidValue;
-  LinParams p{};
-  p.M = L.M;
-  p.N = L.N;
-  p.K = L.K;
-  p.tiles_m = plan.tiles_m;
-  p.tiles_n = plan.tiles_n;
-  p.splits = plan.splits;
-  p.kb_total = (L.K + 63) / 64;
-  p.kb_split = plan.kb_split;
-  p.partial = L.partial;
-  p.status = L.status;
-  if (plan.splits > 1) {
-    p.wide = L.N % 8 == 0 && (reinterpret_cast<uintptr_t>(L.partial) & 31u) == 0;
-  } else {
+  LinPlan plan[2] = {};
+  lin_plan(L, count, plan);
+  CUtensorMap tm[4];
+  LinParams args = {};
+  args.status = status;
+  long long items = 0;
+  for (int i = 0; i < count; ++i) {
+    LinProblem& p = args.p[i];
+    if (!lin_operand(&tm[2 * i], &p.a_3d, L[i].A, L[i].a_mn, L[i].M, L[i].K, 128, L[i].lda) ||
+        !lin_operand(&tm[2 * i + 1], &p.b_3d, L[i].B, L[i].b_mn, L[i].N, L[i].K, plan[i].bn / 2, L[i].ldb))
+      return cudaErrorInvalidValue;
     auto rows32 = [](const void* at, long long ld, int size) {
       return at == nullptr || (ld * size % 32 == 0 && (reinterpret_cast<uintptr_t>(at) & 31u) == 0);
     };
-    p.wide = rows32(L.e.y, L.e.ldy, L.e.y_f32 ? 4 : 2) && rows32(L.e.z, L.e.ldz, 2) &&
-             rows32(L.e.res, L.e.ldr, L.e.res_f32 ? 4 : 2);
+    p.M = L[i].M;
+    p.N = L[i].N;
+    p.a_mn = L[i].a_mn;
+    p.b_mn = L[i].b_mn;
+    p.bn = plan[i].bn;
+    p.tiles_m = plan[i].tiles_m;
+    p.tiles_n = plan[i].tiles_n;
+    p.splits = plan[i].splits;
+    p.kb_total = (L[i].K + kBk - 1) / kBk;
+    p.kb_split = plan[i].kb_split;
+    p.partial = partial;
+    partial += lin_partial(plan[i]);
+    p.e = L[i].e;
+    p.wide = rows32(p.e.y, p.e.ldy, p.e.y_f32 ? 4 : 2) && rows32(p.e.z, p.e.ldz, 2) &&
+             rows32(p.e.res, p.e.ldr, p.e.res_f32 ? 4 : 2);
+    items += static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits;
+    if (items > (1ll << 30)) return cudaErrorInvalidValue;
+    args.end[i] = static_cast<int>(items);
   }
-  p.e = L.e;
-  const long long items = static_cast<long long>(plan.tiles_m) * plan.tiles_n * plan.splits;
-  const int pairs = items < max_pairs_cache[dev] ? static_cast<int>(items) : max_pairs_cache[dev];
-  linear_gemm_kernel<AMN, BMN, BN><<<2 * pairs, kLinThreads, Cfg::SMEM_BYTES, stream>>>(tmA, tmB, p);
+  if (count == 1) {
+    tm[2] = tm[0];
+    tm[3] = tm[1];
+    args.end[1] = args.end[0];
+  }
+  const int pairs = args.end[1] < max_pairs_cache[dev] ? args.end[1] : max_pairs_cache[dev];
+  linear_gemm_kernel<<<2 * pairs, kLinThreads, kLinSmem, stream>>>(tm[0], tm[1], tm[2], tm[3], args);
   e = cudaGetLastError();
-  if (e != cudaSuccess || plan.splits == 1) return e;
-  const unsigned rows = (static_cast<unsigned>(L.M) + 3) / 4;
-  linear_join_kernel<<<dim3((static_cast<unsigned>(L.N) + 63) / 64, rows < 16384 ? rows : 16384), dim3(64, 4), 0,
-                       stream>>>(L.partial, plan.splits, L.M, L.N, L.e);
-  return cudaGetLastError();
+  for (int i = 0; i < count && e == cudaSuccess; ++i) {
+    const LinProblem& p = args.p[i];
+    if (p.splits == 1) continue;
+    const int tiles = p.tiles_m * p.tiles_n;
+    for (int first = 0; first < tiles && e == cudaSuccess; first += 65535) {  // (grid.y's limit)
+      const int n = tiles - first < 65535 ? tiles - first : 65535;
+      linear_join_kernel<<<dim3(8, static_cast<unsigned>(n)), dim3(32, 8), 0, stream>>>(p, first);
+      e = cudaGetLastError();
+    }
+  }
+  return e;
 }
 
-}  // namespace
-
-long long linear_gemm_partial(int M, int N, int K, int y_f32) {
-  const LinPlan p = lin_plan(M, N, K, y_f32);
-  return p.splits > 1 ? static_cast<long long>(p.splits) * M * N : 0;
-}
-
-cudaError_t launch_linear_gemm(const LinearLaunch& L, cudaStream_t stream) {
-  const LinPlan p = lin_plan(L.M, L.N, L.K, L.e.y_f32);
-  if (L.a_mn)
-    return p.bn == 256 ? run_gemm<true, true, 256>(L, p, stream) : run_gemm<true, true, 128>(L, p, stream);
-  if (L.b_mn)
-    return p.bn == 256 ? run_gemm<false, true, 256>(L, p, stream) : run_gemm<false, true, 128>(L, p, stream);
-  return p.bn == 256 ? run_gemm<false, false, 256>(L, p, stream) : run_gemm<false, false, 128>(L, p, stream);
-}
-
-int linear_dz_lines(int M) {
-  const int n = (M + kDzRows - 1) / kDzRows;
-  return n < kDzLines ? n : kDzLines;
+// Lines (blocks along M) that give about four blocks an SM, of at least 8 rows.
+int linear_dz_lines(int M, int N) {
+  const int cols = (N + 255) / 256 > 0 ? (N + 255) / 256 : 1;
+  int n = (4 * device_sm_count() + cols - 1) / cols;
+  if (n > (M + 7) / 8) n = (M + 7) / 8;
+  if (n > kDzLines) n = kDzLines;
+  return n > 0 ? n : 1;
 }
 
 cudaError_t launch_linear_dz(const LinearDzLaunch& L, cudaStream_t stream) {
-  const int lines = linear_dz_lines(L.M);
+  const int lines = linear_dz_lines(L.M, L.N);
   auto rows16 = [](const void* at, long long ld, int size) {
     return at == nullptr || (ld * size % 16 == 0 && (reinterpret_cast<uintptr_t>(at) & 15u) == 0);
   };

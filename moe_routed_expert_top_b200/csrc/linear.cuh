@@ -11,14 +11,43 @@
 
 namespace moe {
 
+// The activations decide an epilogue's time (a 128 x 256 tile is 1000 values a
+// thread quad), so they use the fast exponential and division: relative errors
+// of about 1e-6, a hundredth of a bf16 rounding.
+
+// 1 / (1 + e^-z)
+__device__ __forceinline__ float linear_sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// Phi(z), the normal distribution function, and E = e^(-z^2/2) that its density
+// shares. Phi(-a) = t Q(t) e^(-a^2/2) with t = 1 / (1 + 0.2687 a) for a >= 0: Q, of
+// degree 8, was fitted for this file by weighted least squares to the scaled
+// complementary error function, with 2e-8 of relative error over a <= 18 (beyond,
+// E is 0 in float). In float the relative error is 8e-7 for z >= -5, tails included.
+__device__ __forceinline__ float linear_phi(float z, float& E) {
+  const float t = __fdividef(1.0f, fmaf(0.26870057f, fabsf(z), 1.0f));
+  float q = 0.029524624f;
+  q = fmaf(q, t, -0.13134865f);
+  q = fmaf(q, t, 0.18237928f);
+  q = fmaf(q, t, -0.08126708f);
+  q = fmaf(q, t, 0.11540328f);
+  q = fmaf(q, t, 0.069148935f);
+  q = fmaf(q, t, 0.10200123f);
+  q = fmaf(q, t, 0.10695248f);
+  q = fmaf(q, t, 0.107205935f);
+  E = __expf(-0.5f * z * z);
+  const float tail = q * t * E;
+  return z < 0.0f ? tail : 1.0f - tail;
+}
+
 __device__ __forceinline__ float linear_act(float z, int act) {
+  float E;
   switch (act) {
     case kActRelu:
       return z < 0.0f ? 0.0f : z;  // a NaN stays one
     case kActSilu:
-      return z / (1.0f + expf(-z));
+      return z * linear_sigmoid(z);
     case kActGelu:
-      return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+      return z * linear_phi(z, E);
     default:
       return z;
   }
@@ -26,16 +55,18 @@ __device__ __forceinline__ float linear_act(float z, int act) {
 
 // d act(z) / dz. silu: s (1 + z (1 - s)), s = 1 / (1 + e^-z); gelu: Phi(z) + z phi(z).
 __device__ __forceinline__ float linear_slope(float z, int act) {
+  float E;
   switch (act) {
     case kActRelu:
       return z > 0.0f ? 1.0f : 0.0f;
     case kActSilu: {
-      const float s = 1.0f / (1.0f + expf(-z));
+      const float s = linear_sigmoid(z);
       return s * (1.0f + z * (1.0f - s));
     }
-    case kActGelu:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-             z * expf(-0.5f * z * z) * 0.39894228040143268f;
+    case kActGelu: {
+      const float phi = linear_phi(z, E);
+      return fmaf(z * E, 0.39894228f, phi);
+    }
     default:
       return 1.0f;
   }

@@ -217,7 +217,7 @@ cudaError_t run_few(LinearFewParams p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_linear_few(const LinearLaunch& L, cudaStream_t stream) {
+cudaError_t launch_linear_few(const LinearProduct& L, int32_t* status, cudaStream_t stream) {
   LinearFewParams p = {};
   p.M = L.M;
   p.N = L.N;
@@ -227,7 +227,7 @@ cudaError_t launch_linear_few(const LinearLaunch& L, cudaStream_t stream) {
   p.x = static_cast<const __nv_bfloat16*>(L.A);
   p.w = static_cast<const __nv_bfloat16*>(L.B);
   p.e = L.e;
-  p.status = L.status;
+  p.status = status;
   if (p.M <= 8) return run_few<1>(p, stream);
   if (p.M <= 16) return run_few<2>(p, stream);
   return run_few<4>(p, stream);
