@@ -53,14 +53,15 @@ namespace {
 constexpr int kLinThreads = 320;  // TMA, MMA, two groups of 4 epilogue warps
 constexpr int kMaxBn = 256;
 constexpr int kBk = 128;                         // k of a stage
-constexpr int kStages = 3;
+constexpr int kMaxStages = 6;
 constexpr int kStageA = 128 * kBk * 2;           // this CTA's 128 rows of A
-constexpr int kStageB = (kMaxBn / 2) * kBk * 2;  // its half of B's rows
+// the ring: 3 stages of 64 KB at 256 columns, 4 of 48 KB at 128, ...
+constexpr int kRing = 3 * (kStageA + (kMaxBn / 2) * kBk * 2);
 constexpr int kNumAcc = 2;
 // each epilogue warp's 32 x 16 block (its rows 17 apart) and 128 bias values
 constexpr int kBlockFloats = 32 * 17 + 128;
-constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 1;
-constexpr int kLinSmem = 1024 + kStages * (kStageA + kStageB) + 8 * kBlockFloats * 4 + kNumBars * 8 + 32;
+constexpr int kNumBars = 2 * kMaxStages + 2 * kNumAcc + 1;
+constexpr int kLinSmem = 1024 + kRing + 8 * kBlockFloats * 4 + kNumBars * 8 + 32;
 static_assert(kLinSmem <= 227 * 1024, "shared memory");
 
 // One product: C[m,n] = epilogue(sum_k A(m,k) B(n,k)).
@@ -79,6 +80,7 @@ struct LinProblem {
 struct LinParams {
   LinProblem p[2];
   int end[2];  // work items up to the end of each product
+  int stages, stage_bytes;
   int32_t* status;
 };
 
@@ -233,16 +235,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + kStages * kStageA;
-  float* sBlock = reinterpret_cast<float*>(sB + kStages * kStageB);
+  const int stages = args.stages, stage_bytes = args.stage_bytes;
+  float* sBlock = reinterpret_cast<float*>(smem + kRing);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sBlock + 8 * kBlockFloats);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const uint32_t full0 = smem_u32(bars);
-  const uint32_t empty0 = full0 + 8 * kStages;
-  const uint32_t tfull0 = empty0 + 8 * kStages;
+  const uint32_t empty0 = full0 + 8 * kMaxStages;
+  const uint32_t tfull0 = empty0 + 8 * kMaxStages;
   const uint32_t tempty0 = tfull0 + 8 * kNumAcc;
   const uint32_t drain_bar = tempty0 + 8 * kNumAcc;
 
@@ -255,9 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   int32_t* status = args.status;
 
   if (threadIdx.x == 0) {
-    // (a wait gives up after seconds, long after this)
-    if (blockIdx.x == 0) *status = 0;
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
@@ -276,6 +275,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), kNumAcc * kMaxBn);
+  // what follows reads what earlier kernels of the stream wrote
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;  // (a wait gives up after seconds, long after this)
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or load completion
@@ -308,12 +311,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           const uint32_t fb_local = full0 + 8 * stage;
           const uint32_t fb = cluster_map_shared(fb_local, 0);
           if (leader) mbar_arrive_expect_tx(fb_local, 2u * bytes);
-          const uint32_t a_dst = smem_u32(sA + stage * kStageA);
-          const uint32_t b_dst = smem_u32(sB + stage * kStageB);
+          const uint32_t a_dst = smem_u32(smem) + stage * stage_bytes;
+          const uint32_t b_dst = a_dst + kStageA;
           lin_load(a_dst, tmA, a_mn, a_3d, m0, 128, kb * kBk, fb, pol);
           lin_load(b_dst, tmB, b_mn, b_3d, n0, half, kb * kBk, fb, pol);
           ++issued;
-          if (++stage == kStages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -325,22 +328,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         // both halves' bytes); the other CTA waits for the stages' release. One
         // deadline bounds the drain, the cluster barrier at the end keeps both
         // CTAs alive until both have drained.
-        const uint32_t n = issued < static_cast<uint32_t>(kStages) ? issued : kStages;
+        const uint32_t n = issued < static_cast<uint32_t>(stages) ? issued : static_cast<uint32_t>(stages);
         const uint64_t deadline = globaltimer_ns() + kWaitLimitNs;
         int s = stage;
         uint32_t ph = phase;
         for (uint32_t i = 0; i < n; ++i) {
           if (--s < 0) {
-            s = kStages - 1;
+            s = stages - 1;
             ph ^= 1u;
           }
           mbar_wait_until((leader ? full0 : empty0) + 8 * s, ph, deadline);
         }
       } else {
         // every load this CTA issued has been consumed (its stage released) before leaving
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < stages; ++i) {
           mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, status);
-          if (++stage == kStages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -374,8 +377,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a_at = smem_u32(sA + stage * kStageA);
-          const uint32_t b_at = smem_u32(sB + stage * kStageB);
+          const uint32_t a_at = smem_u32(smem) + stage * stage_bytes;
+          const uint32_t b_at = a_at + kStageA;
           const uint64_t adesc = a_mn ? smem_desc_mn(a_at) : smem_desc_sw128(a_at);
           const uint64_t bdesc = b_mn ? smem_desc_mn(b_at) : smem_desc_sw128(b_at);
 #pragma unroll
@@ -383,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             mma_bf16_pair(d, adesc + a_step * (k & 3) + a_half * (k >> 2),
                           bdesc + b_step * (k & 3) + b_half * (k >> 2), idesc, (kb | k) != 0 ? 1u : 0u);
           mma_commit_pair_mc(empty0 + 8 * stage, 0x3);
-          if (++stage == kStages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -452,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         const int cols = min(32, width - j);
         const float* b = bias + (j >> 6) * 32;
         if (sums) {
-          lin_store32_f32(it.partial + (r0 + lane) * p.bn + j, v);
+          if (lane < rows) lin_store32_f32(it.partial + (r0 + lane) * p.bn + j, v);
         } else if (p.wide && cols == 32) {
           uint32_t now[16];
 #pragma unroll
@@ -516,74 +519,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   }
 }
 
-// y of the tiles computed in parts: the parts' sums, in order. A block has 32 rows
-// of one tile, a thread 8 columns of 4 of them (8 loads in flight a part: with
-// one value a thread the kernel was bound by latency, 19 us against 6 for 34
-// tiles in 2 parts).
+// y of the tiles computed in parts: the parts' sums, in order. A block has 8 rows
+// of one tile, a thread 8 columns of one, and the loads of 4 parts in flight.
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinProblem p, int first) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tile = first + blockIdx.y;
   int tm, tn;
   lin_tile(p, tile, tm, tn);
   const int c = threadIdx.x * 8, n = tn * p.bn + c;
-  const int row0 = blockIdx.x * 32 + threadIdx.y;
-  const long long m0 = static_cast<long long>(tm) * 256 + row0;
-  if (c >= p.bn || n >= p.N || m0 >= p.M) return;
+  const int row = blockIdx.x * 8 + threadIdx.y;
+  const long long m = static_cast<long long>(tm) * 256 + row;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c >= p.bn || n >= p.N || m >= p.M) return;
   const long long step = static_cast<long long>(p.tiles_m) * p.tiles_n * 256 * p.bn;
-  const float* src = p.partial + (static_cast<long long>(tile) * 256 + row0) * p.bn + c;
-  float s[4][8] = {};
-  for (int k = 0; k < p.splits; ++k, src += step) {
+  const float* src = p.partial + (static_cast<long long>(tile) * 256 + row) * p.bn + c;
+  const int cols = min(8, p.N - n);
+  const bool fast = p.wide && cols == 8 && !p.e.y_f32 && (p.e.res == nullptr || !p.e.res_f32);
+  float bias[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) bias[j] = j < cols ? linear_bias(p.e, n + j) : 0.0f;
+  uint4 res = make_uint4(0u, 0u, 0u, 0u);
+  if (fast && p.e.res != nullptr)
+    res = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.e.res) + m * p.e.ldr + n);
+  float s[8] = {};
+  for (int k0 = 0; k0 < p.splits; k0 += 4) {
     float4 v[4][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // (rows past M were written too)
-      v[i][0] = *reinterpret_cast<const float4*>(src + i * 8 * p.bn);
-      v[i][1] = *reinterpret_cast<const float4*>(src + i * 8 * p.bn + 4);
+    for (int i = 0; i < 4; ++i) {
+      v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k0 + i < p.splits) {
+        v[i][0] = *reinterpret_cast<const float4*>(src + (k0 + i) * step);
+        v[i][1] = *reinterpret_cast<const float4*>(src + (k0 + i) * step + 4);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        s[i][4 * j] += v[i][j].x;
-        s[i][4 * j + 1] += v[i][j].y;
-        s[i][4 * j + 2] += v[i][j].z;
-        s[i][4 * j + 3] += v[i][j].w;
+        s[4 * j] += v[i][j].x;
+        s[4 * j + 1] += v[i][j].y;
+        s[4 * j + 2] += v[i][j].z;
+        s[4 * j + 3] += v[i][j].w;
       }
   }
-  const int cols = min(8, p.N - n);
-  float bias[8];
+  if (fast) {
+    const uint32_t rw[4] = {res.x, res.y, res.z, res.w};
+    float y[8], z[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) bias[j] = j < cols ? linear_bias(p.e, n + j) : 0.0f;
-  const bool fast = p.wide && cols == 8 && !p.e.y_f32 && (p.e.res == nullptr || !p.e.res_f32);
+    for (int j = 0; j < 8; ++j)
+      y[j] = linear_result(p.e, s[j], bias[j], j & 1 ? bf16hi_to_f32(rw[j >> 1]) : bf16lo_to_f32(rw[j >> 1]),
+                           &z[j]);
+    if (p.e.z != nullptr)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.e.z) + m * p.e.ldz + n) =
+          make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                     pack_bf16x2(z[6], z[7]));
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.e.y) + m * p.e.ldy + n) =
+        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                   pack_bf16x2(y[6], y[7]));
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long m = m0 + 8 * i;
-    if (m >= p.M) break;
-    if (fast) {
-      uint4 res = make_uint4(0u, 0u, 0u, 0u);
-      if (p.e.res != nullptr)
-        res = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.e.res) + m * p.e.ldr + n);
-      const uint32_t rw[4] = {res.x, res.y, res.z, res.w};
-      float y[8], z[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        y[j] = linear_result(p.e, s[i][j], bias[j], j & 1 ? bf16hi_to_f32(rw[j >> 1]) : bf16lo_to_f32(rw[j >> 1]),
-                             &z[j]);
-      if (p.e.z != nullptr)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.e.z) + m * p.e.ldz + n) =
-            make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
-                       pack_bf16x2(z[6], z[7]));
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.e.y) + m * p.e.ldy + n) =
-          make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                     pack_bf16x2(y[6], y[7]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < cols) {
-          float z;
-          const float y = linear_result(p.e, s[i][j], bias[j],
-                                        p.e.res != nullptr ? linear_res(p.e, m, n + j) : 0.0f, &z);
-          linear_put(p.e, m, n + j, y, z);
-        }
-    }
+    for (int j = 0; j < 8; ++j)
+      if (j < cols) {
+        float z;
+        const float y = linear_result(p.e, s[j], bias[j], p.e.res != nullptr ? linear_res(p.e, m, n + j) : 0.0f, &z);
+        linear_put(p.e, m, n + j, y, z);
+      }
   }
 }
 
@@ -696,7 +696,7 @@ bool lin_encode3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t ro
 // An operand of `out` output indices and K, of which a stage takes `rows` and 128.
 bool lin_operand(CUtensorMap* map, int* three, const void* base, int mn, int out, int K, int rows, long long ld) {
   const int inner = mn ? out : K;
-  *three = inner % 64 == 0;
+  *three = inner % 64 == 0 && (!mn || rows % 64 == 0);  // (mn: copies start at whole blocks)
   if (*three)
     return mn ? lin_encode3(map, base, out, K, kBk, (rows + 63) / 64, ld)
               : lin_encode3(map, base, K, out, rows, kBk / 64, ld);
@@ -711,23 +711,22 @@ struct LinPlan {
 // With a tile for every pair: whole tiles of 256 x 256. (An output that leaves part
 // of the last turn idle is no slower for it: the operands' way from L2 is shared
 // by all, and cutting the last turn's tiles along k measured the same.) With
-// fewer: the tiles are cut along k into parts of g blocks that fill the pairs, or
-// are 128 wide, or both, whichever has the least modelled time in SM clocks: a
-// 128-wide k block takes about 800 + 2.4 bn, a tile 1500 that the next one does not
-// hide, and the parts' sums are written, read and added once. An fp32 result is
-// made of parts of at most 16 blocks (2048 k) throughout.
+// fewer: the tiles are cut along k into parts of g blocks, or are 128 or 64 wide,
+// or both, whichever has the least modelled time in SM clocks: a 128-wide k block
+// takes about 800 + 2.4 bn, an item 3000 beside its blocks, and parts a second
+// kernel, their sums written, read and added. An fp32 result is made of parts of
+// at most 16 blocks (2048 k) throughout.
 void lin_plan(const LinearProduct* L, int count, LinPlan* out) {
   const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
   double best = -1.0;
-  for (int narrow = 0; narrow < 2; ++narrow) {
+  for (int width = kMaxBn; width >= 64; width /= 2) {
     LinPlan p[2] = {};
-    int kb[2] = {0, 0}, kb_most = 0, bn = 0;
+    int kb[2] = {0, 0}, kb_most = 0;
     long long tiles = 0;
     bool fp32 = false;
     for (int i = 0; i < count; ++i) {
-      const int n32 = (L[i].N + 31) / 32 * 32, most = narrow ? 128 : 256;
-      p[i].bn = n32 < most ? n32 : most;
-      if (p[i].bn > bn) bn = p[i].bn;
+      const int n32 = (L[i].N + 31) / 32 * 32;
+      p[i].bn = n32 < width ? n32 : width;
       p[i].tiles_m = (L[i].M + 255) / 256;
       p[i].tiles_n = (L[i].N + p[i].bn - 1) / p[i].bn;
       kb[i] = (L[i].K + kBk - 1) / kBk;
@@ -741,26 +740,28 @@ void lin_plan(const LinearProduct* L, int count, LinPlan* out) {
       const int g = (kb_most + cut - 1) / cut;
       if (cut > least && g < 2) break;
       long long items = 0;
-      double bytes = 0.0;
+      double bytes = 0.0, all = 0.0, longest = 0.0;
       LinPlan q[2] = {p[0], p[1]};
       for (int i = 0; i < count; ++i) {
         q[i].splits = (kb[i] + g - 1) / g;
         q[i].kb_split = (kb[i] + q[i].splits - 1) / q[i].splits;
         q[i].splits = (kb[i] + q[i].kb_split - 1) / q[i].kb_split;
         const long long n = static_cast<long long>(q[i].tiles_m) * q[i].tiles_n * q[i].splits;
+        const double one = q[i].kb_split * (800.0 + 2.4 * q[i].bn) + 3000.0;
         items += n;
+        all += n * one;
+        if (one > longest) longest = one;
         if (q[i].splits > 1) bytes += 8.0 * n * 256.0 * q[i].bn;
       }
-      const long long turns = (items + pairs - 1) / pairs;
-      double t = static_cast<double>(turns) * (g * (800.0 + 2.4 * bn) + 1500.0);
-      if (bytes > 0.0) t += 5000.0 + bytes / 3400.0;
+      double t = items <= pairs ? longest : all / pairs + 0.5 * longest;
+      if (bytes > 0.0) t += 6000.0 + bytes / 3400.0;
       if (best < 0.0 || t < best) {
         best = t;
         out[0] = q[0];
         out[1] = q[1];
       }
     }
-    if (!narrow && tiles >= pairs) break;
+    if (tiles >= pairs) break;
   }
 }
 
@@ -835,17 +836,36 @@ cudaError_t launch_linear_gemm(const LinearProduct* L, int count, float* partial
     tm[3] = tm[1];
     args.end[1] = args.end[0];
   }
+  int bn = 32;
+  for (int i = 0; i < count; ++i)
+    if (plan[i].bn > bn) bn = plan[i].bn;
+  // (a b_mn operand comes in blocks of 64 output indices)
+  args.stage_bytes = kStageA + (bn / 2 + 63) / 64 * 64 * kBk * 2;
+  args.stages = kRing / args.stage_bytes < kMaxStages ? kRing / args.stage_bytes : kMaxStages;
   const int pairs = args.end[1] < max_pairs_cache[dev] ? args.end[1] : max_pairs_cache[dev];
-  linear_gemm_kernel<<<2 * pairs, kLinThreads, kLinSmem, stream>>>(tm[0], tm[1], tm[2], tm[3], args);
-  e = cudaGetLastError();
+  // Both kernels may be launched while the kernel before them ends (their work
+  // waits for it): a launch's latency is as long as a small product.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = kLinSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel, tm[0], tm[1], tm[2], tm[3], args);
   for (int i = 0; i < count && e == cudaSuccess; ++i) {
     const LinProblem& p = args.p[i];
     if (p.splits == 1) continue;
     const int tiles = p.tiles_m * p.tiles_n;
     for (int first = 0; first < tiles && e == cudaSuccess; first += 65535) {  // (grid.y's limit)
       const int n = tiles - first < 65535 ? tiles - first : 65535;
-      linear_join_kernel<<<dim3(8, static_cast<unsigned>(n)), dim3(32, 8), 0, stream>>>(p, first);
-      e = cudaGetLastError();
+      cfg.gridDim = dim3(p.M < 256 ? (static_cast<unsigned>(p.M) + 7) / 8 : 32, static_cast<unsigned>(n));
+      cfg.blockDim = dim3(32, 8);
+      cfg.dynamicSmemBytes = 0;
+      e = cudaLaunchKernelEx(&cfg, linear_join_kernel, p, first);
     }
   }
   return e;

@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(256) sum_lines_kernel(const float* partial, in
   const float* src = partial + static_cast<long long>(blockIdx.y) * lines * H + c;
   float s = 0.0f;
   if (c < H)
+#pragma unroll 8
     for (int l = w; l < lines; l += 8) s += src[static_cast<long long>(l) * H];
   sum[w][lane] = s;
   __syncthreads();
