@@ -398,12 +398,12 @@ def moe_experts_forward_few(prob, hidden, logits, topk_ids, topk_weights, w_gate
                             stream=None):
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib().moe_experts_forward_few(ctypes.byref(prob), _ptr(hidden), _ptr(logits),
-                                         _ptr(topk_ids), _ptr(topk_weights), _ptr(w_gate_up),
-                                         _ptr(w_down), _ptr(ws_gate_up), _ptr(ws_down),
-                                         float(scale), _ptr(residual), _ptr(out), _ptr(workspace),
-                                         int(ws_bytes), _stream(stream)),
-           "moe_experts_forward_few")
+    status = lib().moe_experts_forward_few(
+        ctypes.byref(prob), _ptr(hidden), _ptr(logits), _ptr(topk_ids), _ptr(topk_weights),
+        _ptr(w_gate_up), _ptr(w_down), _ptr(ws_gate_up), _ptr(ws_down), scale, _ptr(residual),
+        _ptr(out), _ptr(workspace), ws_bytes, _stream(stream))
+    if status:
+        _check(status, "moe_experts_forward_few")
 
 
 def moe_linear_workspace_bytes(desc: LinearDesc) -> int:
@@ -413,9 +413,10 @@ def moe_linear_workspace_bytes(desc: LinearDesc) -> int:
 def moe_linear(desc, x, w, bias, residual, y, z, workspace, ws_bytes=None, stream=None):
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib().moe_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
-                            _ptr(y), _ptr(z), _ptr(workspace), int(ws_bytes), _stream(stream)),
-           "moe_linear")
+    status = lib().moe_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
+                              _ptr(y), _ptr(z), _ptr(workspace), ws_bytes, _stream(stream))
+    if status:
+        _check(status, "moe_linear")
 
 
 def moe_linear_backward_workspace_bytes(desc: LinearDesc) -> int:
@@ -425,17 +426,19 @@ def moe_linear_backward_workspace_bytes(desc: LinearDesc) -> int:
 def moe_linear_backward(desc, dy, x, w, z, dx, dw, dbias, workspace, ws_bytes=None, stream=None):
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib().moe_linear_backward(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(w), _ptr(z),
-                                     _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(workspace),
-                                     int(ws_bytes), _stream(stream)), "moe_linear_backward")
+    status = lib().moe_linear_backward(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(w), _ptr(z),
+                                       _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(workspace), ws_bytes,
+                                       _stream(stream))
+    if status:
+        _check(status, "moe_linear_backward")
 
 
 def moe_layer_norm(M, H, ldx, ldy, x_f32, w_f32, x, gamma, beta, eps, y, mean=None, rstd=None,
                    stream=None):
-    _check(lib().moe_layer_norm(int(M), int(H), int(ldx), int(ldy), int(bool(x_f32)),
-                                int(bool(w_f32)), _ptr(x), _ptr(gamma), _ptr(beta), float(eps),
-                                _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream)),
-           "moe_layer_norm")
+    status = lib().moe_layer_norm(M, H, ldx, ldy, x_f32, w_f32, _ptr(x), _ptr(gamma), _ptr(beta),
+                                  eps, _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream))
+    if status:
+        _check(status, "moe_layer_norm")
 
 
 def moe_layer_norm_backward_workspace_bytes(M, H) -> int:
@@ -446,12 +449,12 @@ def moe_layer_norm_backward(M, H, lddy, ldx, lddx, x_f32, w_f32, dy, x, gamma, m
                             dgamma, dbeta, workspace=None, ws_bytes=None, stream=None):
     if ws_bytes is None:
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().moe_layer_norm_backward(int(M), int(H), int(lddy), int(ldx), int(lddx),
-                                         int(bool(x_f32)), int(bool(w_f32)), _ptr(dy), _ptr(x),
-                                         _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
-                                         _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
-                                         int(ws_bytes), _stream(stream)),
-           "moe_layer_norm_backward")
+    status = lib().moe_layer_norm_backward(M, H, lddy, ldx, lddx, x_f32, w_f32, _ptr(dy), _ptr(x),
+                                           _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
+                                           _ptr(dgamma), _ptr(dbeta), _ptr(workspace), ws_bytes,
+                                           _stream(stream))
+    if status:
+        _check(status, "moe_layer_norm_backward")
 
 
 def moe_decode_device_status(dev_status: int) -> int:

@@ -174,29 +174,48 @@ _SAME_DEVICE = contextlib.nullcontext()
 def _on_device_of(t: torch.Tensor):
     """Context in which the tensor's device is the current one: the library
     launches on the current device and its current stream."""
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    if t.device.index == torch.cuda.current_device():
+    if t.get_device() == torch.cuda.current_device():
         return _SAME_DEVICE
     return torch.cuda.device(t.device)
 
 
+def _stream_of(t: torch.Tensor) -> int:
+    """The current stream of the tensor's device. (Asked for by index: without one,
+    torch takes longer to find the index than the rest of a small call.)"""
+    return torch.cuda.current_stream(t.get_device()).cuda_stream
+
+
 def _matrix(t: torch.Tensor, name: str, shape, dtypes, device) -> int:
-    """Checks a matrix whose rows are dense; returns its row pitch (0 where one
-    row or less leaves it open)."""
-    if not torch.is_tensor(t) or t.dim() != 2 or tuple(t.shape) != tuple(shape):
+    """Checks a matrix whose rows are dense; returns its row pitch (0: the rows
+    follow one another, or one row or less leaves it open)."""
+    if not torch.is_tensor(t) or t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.is_contiguous():
+        return 0
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} needs rows of stride 1")
-    if t.shape[0] <= 1 or t.shape[1] == 0:
+    if t.shape[0] <= 1:
         return 0
     if t.stride(0) < t.shape[1]:
         raise ValueError(f"{name}'s rows overlap")
     return t.stride(0)
+
+
+def _remember(cache: dict, key, value):
+    """Keeps a call's descriptor for the next call of the same sizes."""
+    if len(cache) >= 256:
+        cache.clear()
+    cache[key] = value
+    return value
+
+
+_BF16, _F32, _EITHER = (torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32)
 
 
 def _vector(t: torch.Tensor | None, name: str, n: int, device):
@@ -247,6 +266,12 @@ class FewTokenExperts:
                             score_fn=self.score_fn, renormalize=self.renormalize,
                             routed_scaling_factor=self.scale, F_shared=self.F_shared)
 
+    def _dense(self, t, name, T, cols, dtype):
+        if t.dtype != dtype or t.shape != (T, cols) or t.device != self.device:
+            raise ValueError(f"{name} must be {dtype} [{T}, {cols}] on {self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
     def forward(self, hidden: torch.Tensor, topk_ids: torch.Tensor | None = None,
                 topk_weights: torch.Tensor | None = None, logits: torch.Tensor | None = None,
                 residual: torch.Tensor | None = None,
@@ -257,31 +282,30 @@ class FewTokenExperts:
         T = hidden.shape[0]
         if T > MOE_FEW_MAX_TOKENS:
             raise ValueError(f"at most {MOE_FEW_MAX_TOKENS} tokens, not {T}: use RoutedExperts")
-        for t, name, cols, dtype in ((hidden, "hidden", self.H, torch.bfloat16),
-                                     (logits, "logits", self.E, torch.float32),
-                                     (topk_ids, "topk_ids", self.top_k, torch.int32),
-                                     (topk_weights, "topk_weights", self.top_k, torch.float32),
-                                     (residual, "residual", self.H, torch.bfloat16),
-                                     (out, "out", self.H, torch.bfloat16)):
-            if t is None:
-                continue
-            if t.dtype != dtype or t.shape != (T, cols) or t.device != self.device:
-                raise ValueError(f"{name} must be {dtype} [{T}, {cols}] on {self.device}")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+        self._dense(hidden, "hidden", T, self.H, torch.bfloat16)
+        if logits is not None:
+            self._dense(logits, "logits", T, self.E, torch.float32)
+        if topk_ids is not None:
+            self._dense(topk_ids, "topk_ids", T, self.top_k, torch.int32)
+        if topk_weights is not None:
+            self._dense(topk_weights, "topk_weights", T, self.top_k, torch.float32)
+        if residual is not None:
+            self._dense(residual, "residual", T, self.H, torch.bfloat16)
+        if out is not None:
+            self._dense(out, "out", T, self.H, torch.bfloat16)
         if logits is None and (topk_ids is None or topk_weights is None):
             raise ValueError("need logits, or topk_ids and topk_weights")
         known = self._problems.get(T)
         if known is None:
             prob = self.problem(T)
-            known = self._problems[T] = (prob, moe_few_workspace_bytes(prob))
+            known = self._problems[T] = (prob, max(moe_few_workspace_bytes(prob), 1024))
         with _on_device_of(hidden):
             if out is None:
                 out = torch.empty_like(hidden)
-            self._ws = ws = torch.empty(max(known[1], 1024), dtype=torch.uint8, device=self.device)
+            self._ws = ws = torch.empty(known[1], dtype=torch.uint8, device=self.device)
             moe_experts_forward_few(known[0], hidden, logits, topk_ids, topk_weights,
                                     self.w_gate_up, self.w_down, self.ws_gate_up, self.ws_down,
-                                    self.scale, residual, out, ws, ws.shape[0])
+                                    self.scale, residual, out, ws, known[1], _stream_of(hidden))
         return out
 
     def device_status(self) -> int:
@@ -304,16 +328,25 @@ class Linear:
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("out_dtype must be bfloat16 or float32")
         self.device = weight.device
-        self.ldw = _matrix(weight, "weight", weight.shape, (torch.bfloat16,), self.device)
+        self.ldw = _matrix(weight, "weight", weight.shape, _BF16, self.device)
         self.weight = weight
         self.bias = _vector(bias, "bias", self.N, self.device)
         self.activation, self.out_dtype = activation, out_dtype
+        self._out = (out_dtype,)
+        self._descs = {}
         self._ws = None
 
-    def _desc(self, M, ldx=0, ldr=0, ldy=0, ldz=0, res_f32=False):
-        return make_linear_desc(M, self.N, self.K, self.activation,
-                                self.bias is not None and self.bias.dtype == torch.float32, res_f32,
-                                self.out_dtype == torch.float32, ldx, self.ldw, ldr, ldy, ldz)
+    def _desc(self, nbytes, M, ldx, ldr, ldy, ldz, res_f32):
+        """(descriptor, workspace bytes by ``nbytes``) of a call."""
+        key = (nbytes, M, ldx, ldr, ldy, ldz, res_f32)
+        known = self._descs.get(key)
+        if known is None:
+            d = make_linear_desc(M, self.N, self.K, self.activation,
+                                 self.bias is not None and self.bias.dtype == torch.float32,
+                                 res_f32, self.out_dtype == torch.float32, ldx, self.ldw, ldr, ldy,
+                                 ldz)
+            known = _remember(self._descs, key, (d, max(nbytes(d), 1024)))
+        return known
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
                 out: torch.Tensor | None = None, with_z: bool = False):
@@ -321,19 +354,21 @@ class Linear:
         x unless the activation is none."""
         M = x.shape[0]
         dev = self.device
-        ldx = _matrix(x, "x", (M, self.K), (torch.bfloat16,), dev)
-        ldr = 0 if residual is None else _matrix(residual, "residual", (M, self.N),
-                                                 (torch.bfloat16, torch.float32), dev)
-        ldy = 0 if out is None else _matrix(out, "out", (M, self.N), (self.out_dtype,), dev)
+        ldx = _matrix(x, "x", (M, self.K), _BF16, dev)
+        ldr = ldy = 0
+        res_f32 = False
+        if residual is not None:
+            ldr = _matrix(residual, "residual", (M, self.N), _EITHER, dev)
+            res_f32 = residual.dtype == torch.float32
+        if out is not None:
+            ldy = _matrix(out, "out", (M, self.N), self._out, dev)
+        d, need = self._desc(moe_linear_workspace_bytes, M, ldx, ldr, ldy, 0, res_f32)
         with _on_device_of(x):
             if out is None:
                 out = torch.empty(M, self.N, dtype=self.out_dtype, device=dev)
             z = torch.empty(M, self.N, dtype=torch.bfloat16, device=dev) if with_z else None
-            d = self._desc(M, ldx, ldr, ldy, 0, residual is not None and
-                           residual.dtype == torch.float32)
-            need = moe_linear_workspace_bytes(d)
-            self._ws = ws = torch.empty(max(need, 1024), dtype=torch.uint8, device=dev)
-            moe_linear(d, x, self.weight, self.bias, residual, out, z, ws, ws.shape[0])
+            self._ws = ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            moe_linear(d, x, self.weight, self.bias, residual, out, z, ws, need, _stream_of(x))
         return (out, z) if with_z else out
 
     def backward(self, dy: torch.Tensor, x: torch.Tensor, z: torch.Tensor | None = None,
@@ -349,17 +384,16 @@ class Linear:
             raise ValueError("backward of an activation needs the forward's z")
         if self.activation == "none":
             z = None
-        ldy = _matrix(dy, "dy", (M, self.N), (self.out_dtype,), dev)
-        ldx = _matrix(x, "x", (M, self.K), (torch.bfloat16,), dev)
-        ldz = 0 if z is None else _matrix(z, "z", (M, self.N), (torch.bfloat16,), dev)
+        ldy = _matrix(dy, "dy", (M, self.N), self._out, dev)
+        ldx = _matrix(x, "x", (M, self.K), _BF16, dev)
+        ldz = 0 if z is None else _matrix(z, "z", (M, self.N), _BF16, dev)
+        d, need = self._desc(moe_linear_backward_workspace_bytes, M, ldx, 0, ldy, ldz, False)
         with _on_device_of(x):
             dx = torch.empty(M, self.K, dtype=torch.bfloat16, device=dev) if need_dx else None
             dw = torch.empty(self.N, self.K, dtype=torch.bfloat16, device=dev) if need_dw else None
             db = torch.empty(self.N, dtype=torch.float32, device=dev) if need_dbias else None
-            d = self._desc(M, ldx, 0, ldy, ldz)
-            need = moe_linear_backward_workspace_bytes(d)
-            self._ws = ws = torch.empty(max(need, 1024), dtype=torch.uint8, device=dev)
-            moe_linear_backward(d, dy, x, self.weight, z, dx, dw, db, ws, ws.shape[0])
+            self._ws = ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            moe_linear_backward(d, dy, x, self.weight, z, dx, dw, db, ws, need, _stream_of(x))
         return dx, dw, db
 
     def device_status(self) -> int:
@@ -391,7 +425,7 @@ class LayerNorm:
     def _check(self, x: torch.Tensor):
         if x.dim() != 2 or x.shape[1] < 1 or (self.H is not None and x.shape[1] != self.H):
             raise ValueError(f"x must be [M, {'H' if self.H is None else self.H}]")
-        return _matrix(x, "x", x.shape, (torch.bfloat16, torch.float32), self.device or x.device)
+        return _matrix(x, "x", x.shape, _EITHER, self.device or x.device)
 
     def forward(self, x: torch.Tensor, out: torch.Tensor | None = None, stats: bool = False):
         """y, or (y, mean, rstd) with ``stats``: what ``backward`` needs beside x."""
@@ -404,9 +438,9 @@ class LayerNorm:
             mean = rstd = None
             if stats:
                 mean = torch.empty(M, dtype=torch.float32, device=x.device)
-                rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+                rstd = torch.empty_like(mean)
             moe_layer_norm(M, H, ldx, ldy, x.dtype == torch.float32, self.w_f32, x, self.weight,
-                           self.bias, self.eps, out, mean, rstd)
+                           self.bias, self.eps, out, mean, rstd, _stream_of(x))
         return (out, mean, rstd) if stats else out
 
     def backward(self, dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -429,7 +463,7 @@ class LayerNorm:
                 ws = torch.empty(moe_layer_norm_backward_workspace_bytes(M, H), dtype=torch.uint8,
                                  device=x.device)
             moe_layer_norm_backward(M, H, lddy, ldx, 0, x.dtype == torch.float32, self.w_f32, dy, x,
-                                    self.weight, mean, rstd, dx, dw, db, ws)
+                                    self.weight, mean, rstd, dx, dw, db, ws, None, _stream_of(x))
         return dx, dw, db
 
 
