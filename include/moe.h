@@ -543,7 +543,7 @@ moe_status moe_layer_norm(int32_t M, int32_t H, int64_t ldx, int64_t ldy, int32_
  * dy, x, dx as x and y above (pitches lddy, ldx, lddx); mean and rstd as the forward
  * pass wrote them. dx, dgamma and dbeta may be NULL; dx may be dy or x (same pitch).
  * The row sums of the weight gradients go through `workspace` (needed when dgamma or
- * dbeta is given; 16-byte aligned, moe_layer_norm_backward_workspace_bytes), in a
+ * dbeta is given; 32-byte aligned, moe_layer_norm_backward_workspace_bytes), in a
  * fixed order. M == 0 writes zeros into dgamma and dbeta. */
 size_t moe_layer_norm_backward_workspace_bytes(int32_t M, int32_t H);
 moe_status moe_layer_norm_backward(int32_t M, int32_t H, int64_t lddy, int64_t ldx, int64_t lddx,

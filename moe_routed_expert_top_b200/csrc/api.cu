@@ -1178,7 +1178,7 @@ moe_status moe_layer_norm_backward(int32_t M, int32_t H, int64_t lddy, int64_t l
   const unsigned xa = x_f32 ? 4 : 2;
   if (!aligned(dy, xa) || !aligned(x, xa) || !aligned(dx, xa) || !aligned(gamma, w_f32 ? 4 : 2) ||
       !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dbeta, 4) ||
-      !aligned(workspace, 16))
+      !aligned(workspace, 32))
     return MOE_ERR_INVALID_ARG;
   if (M == 0) {  // sums over no rows
     for (float* o : {dgamma, dbeta})

@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -40,6 +41,7 @@ namespace {
 constexpr int kEpt = 16;            // values of a row held by one thread
 constexpr int kNormMaxThreads = 1024;
 constexpr int kNormBwdMaxThreads = 512;
+constexpr int kShortRow = 2048;     // values of a row that shares its block with others, at most
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
@@ -146,7 +148,7 @@ __device__ __forceinline__ void row_stats(const Vec<T, V> (&xv)[kEpt / V], int H
     }
     d2 += (i * blockDim.x + threadIdx.x) * V < H ? t : 0.0f;
   }
-  rstd = 1.0f / sqrtf(row_sum(d2, slot, 1) * inv + eps);
+  rstd = rsqrtf(row_sum(d2, slot, 1) * inv + eps);
 }
 
 template <typename T, typename WT, int V>
@@ -166,20 +168,6 @@ __device__ __forceinline__ void store_row(const NormLaunch& p, long long row, co
       *reinterpret_cast<Vec<T, V>*>(y + c) = o;
     }
   }
-}
-
-constexpr int kNormStages = 8;
-
-// One row of `bytes` (a multiple of 16) into shared memory, counted on `bar`;
-// `first`: of the copies that this phase of the barrier counts, two in all with
-// `both`.
-__device__ __forceinline__ void norm_copy(void* dst, const void* src, uint32_t bytes, uint32_t bar, bool first,
-                                          bool both = false) {
-  if (first) mbar_arrive_expect_tx(bar, both ? 2 * bytes : bytes);
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
 }
 
 template <typename T, typename WT, int V>
@@ -212,53 +200,279 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormLaunch 
   }
 }
 
-// The same for rows of 2 KB and more whose accesses are 16 bytes wide: whole rows
-// come through a ring in shared memory, a bulk copy each, so that 100 KB an SM and
-// more are on their way whatever the threads do (registers hold one row ahead). The
-// block's barrier of a row's first sum tells that all have taken their values; its
-// first thread then asks for the row that goes in that place.
-template <typename T, typename WT>
-__global__ void __launch_bounds__(kNormMaxThreads) norm_ring_kernel(const NormLaunch p, int stages) {
-  constexpr int V = 16 / sizeof(T);
-  constexpr int NV = kEpt / V;
-  using VT = Vec<T, V>;
+// ---------------------------------------------------------------------------
+// Rows of 2 KB and more: whole rows come through a ring in shared memory, a bulk
+// copy each, so that 100 KB an SM and more are on their way whatever the threads
+// do. The block's barrier of a row's first sum tells that all have taken their
+// values; its first thread then asks for the row that goes in that place.
+//
+// A bulk copy takes whole 16-byte pieces. A row that does not begin and end at
+// such pieces (an odd length) is copied with the pieces around it, which belong to
+// its neighbours or to the gap between rows; only the matrix's first and last
+// row can begin or end in a piece that is not all the matrix's, and their few
+// values there are read one by one.
+// ---------------------------------------------------------------------------
+constexpr int kNormStages = 8;
+
+struct NormRows {
+  const uint8_t* base;  // first byte of the matrix
+  const uint8_t* end;   // behind its last
+  long long ld;         // bytes from row to row
+  int bytes;            // of a row
+};
+
+__device__ __forceinline__ const uint8_t* down16(const uint8_t* p) {
+  return reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(15));
+}
+__device__ __forceinline__ const uint8_t* up16(const uint8_t* p) { return down16(p + 15); }
+
+template <typename T>
+__device__ __forceinline__ NormRows norm_rows(const void* x, long long ld, int M, int H) {
+  NormRows r;
+  r.base = static_cast<const uint8_t*>(x);
+  r.ld = ld * static_cast<long long>(sizeof(T));
+  r.bytes = H * static_cast<int>(sizeof(T));
+  r.end = r.base + (M - 1) * r.ld + r.bytes;
+  return r;
+}
+
+// The 16-byte pieces of a row that lie in the matrix: [lo, hi).
+__device__ __forceinline__ void norm_span(const NormRows& r, long long row, const uint8_t*& lo, const uint8_t*& hi) {
+  const uint8_t* at = r.base + row * r.ld;
+  lo = down16(at);
+  hi = up16(at + r.bytes);
+  if (lo < r.base) lo = up16(r.base);
+  if (hi > r.end) hi = down16(r.end);
+}
+
+// Asks for a row (one thread). The row's place in `dst` (16-byte aligned) begins at
+// its address's offset from a 16-byte piece.
+__device__ __forceinline__ uint32_t norm_ask_bytes(const NormRows& r, long long row) {
+  const uint8_t *lo, *hi;
+  norm_span(r, row, lo, hi);
+  return static_cast<uint32_t>(hi - lo);
+}
+__device__ __forceinline__ void norm_ask(const NormRows& r, long long row, uint8_t* dst, uint32_t bar) {
+  const uint8_t *lo, *hi;
+  norm_span(r, row, lo, hi);
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst) + static_cast<uint32_t>(lo - down16(r.base + row * r.ld))),
+               "l"(lo), "r"(static_cast<uint32_t>(hi - lo)), "r"(bar)
+               : "memory");
+}
+
+// The values of the first and last row that no copy brings (whole block; a barrier
+// has to follow).
+template <typename T>
+__device__ __forceinline__ void norm_edges(const NormRows& r, long long row, uint8_t* dst) {
+  const uint8_t *lo, *hi;
+  norm_span(r, row, lo, hi);
+  const uint8_t* at = r.base + row * r.ld;
+  const int n = r.bytes / static_cast<int>(sizeof(T));
+  const int head = lo > at ? static_cast<int>((lo - at) / sizeof(T)) : 0;
+  const int tail = hi < at + r.bytes ? static_cast<int>((at + r.bytes - hi) / sizeof(T)) : 0;
+  T* out = reinterpret_cast<T*>(dst + (at - down16(at)));
+  const int t = threadIdx.x;
+  if (t < head) out[t] = reinterpret_cast<const T*>(at)[t];
+  if (t < tail) out[n - 1 - t] = reinterpret_cast<const T*>(at)[n - 1 - t];
+}
+
+// ---- two fp32 in one register pair (the row kernels are near the issue rate)
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+__device__ __forceinline__ float2 split(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ float sum(Pair p) {
+  const float2 f = split(p);
+  return f.x + f.y;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// A pair of stored values.
+__device__ __forceinline__ Pair pair_of(const __nv_bfloat16* v) {
+  uint32_t w;
+  memcpy(&w, v, 4);
+  return pair(bf16lo_to_f32(w), bf16hi_to_f32(w));
+}
+__device__ __forceinline__ Pair pair_of(const float* v) { return pair(v[0], v[1]); }
+
+// The thread's 16 values as they are stored, vector i of V values at column
+// (i blockDim.x + threadIdx.x) V (past the row: `absent`), and as 8 pairs. V 1: the
+// pairs are vectors 2k, 2k + 1.
+template <typename T, int V>
+struct Held {
+  Vec<T, V> v[kEpt / V];
+};
+template <typename T, int V>
+__device__ __forceinline__ void take(const T* row, int H, float absent, Held<T, V>& h) {
+#pragma unroll
+  for (int i = 0; i < kEpt / V; ++i) {
+    const int c = (i * blockDim.x + threadIdx.x) * V;
+    if (c < H) {
+      h.v[i] = *reinterpret_cast<const Vec<T, V>*>(row + c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) from_f32(h.v[i].v[j], absent);
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ Pair pair_at(const Held<T, V>& h, int k) {
+  if constexpr (V == 1)
+    return pair(to_f32(h.v[2 * k].v[0]), to_f32(h.v[2 * k + 1].v[0]));
+  else
+    return pair_of(&h.v[k / (V / 2)].v[2 * (k % (V / 2))]);
+}
+
+// Stores the 8 pairs where take found them.
+template <typename T, int V>
+__device__ __forceinline__ void put_pairs(T* row, int H, const Pair (&f)[kEpt / 2]) {
+  if constexpr (V == 1) {
+#pragma unroll
+    for (int k = 0; k < kEpt / 2; ++k) {
+      const int c0 = 2 * k * blockDim.x + threadIdx.x, c1 = c0 + blockDim.x;
+      const float2 p = split(f[k]);
+      if (c0 < H) from_f32(row[c0], p.x);
+      if (c1 < H) from_f32(row[c1], p.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEpt / V; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      if (c < H) {
+        Vec<T, V> v;
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 p = split(f[i * (V / 2) + j]);
+          if constexpr (sizeof(T) == 2) {
+            const uint32_t w = pack_bf16x2(p.x, p.y);
+            memcpy(&v.v[2 * j], &w, 4);
+          } else {
+            v.v[2 * j] = p.x;
+            v.v[2 * j + 1] = p.y;
+          }
+        }
+        *reinterpret_cast<Vec<T, V>*>(row + c) = v;
+      }
+    }
+  }
+}
+
+// kLong: rows of more than 8192 values, whose 1024 threads have 64 registers each.
+// Else a thread keeps its weights over the rows: two blocks of 512 threads share an
+// SM where a kept weight is half a register, one where it is a whole one.
+template <typename T, typename WT, int V>
+constexpr bool kNormSlim = sizeof(T) == 2 && sizeof(WT) == 2 && V > 1;
+template <typename T, typename WT, int V, bool kLong>
+__global__ void __launch_bounds__(kLong ? 1024 : 512, !kLong && kNormSlim<T, WT, V> ? 2 : 1)
+    norm_ring_kernel(const NormLaunch p, int stages, int stage_bytes) {
+  constexpr int NP = kEpt / 2;
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ float slot[2 * 32];
   __shared__ uint64_t bars[kNormStages];
   const float inv = 1.0f / static_cast<float>(p.H);
-  const uint32_t bytes = static_cast<uint32_t>(p.H) * sizeof(T);
-  const T* x = static_cast<const T*>(p.x);
+  const NormRows rows = norm_rows<T>(p.x, p.ldx, p.M, p.H);
+  auto ask = [&](int s, long long row) {
+    if (row >= p.M) return;
+    mbar_arrive_expect_tx(smem_u32(bars + s), norm_ask_bytes(rows, row));
+    norm_ask(rows, row, norm_smem + s * stage_bytes, smem_u32(bars + s));
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(bars + s), 1);
     mbar_fence_init();
-    for (int s = 0; s < stages; ++s) {
-      const long long row = blockIdx.x + static_cast<long long>(s) * gridDim.x;
-      if (row < p.M) norm_copy(norm_smem + s * bytes, x + row * p.ldx, bytes, smem_u32(bars + s), true);
+    for (int s = 0; s < stages; ++s) ask(s, blockIdx.x + static_cast<long long>(s) * gridDim.x);
+  }
+  // the thread's weights: kept, or read (from L1) for each row before its second sum
+  constexpr bool kKeep = !kLong;
+  Held<WT, V> gamma, beta;
+#pragma unroll
+  for (int i = 0; i < kEpt / V; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      from_f32(gamma.v[i].v[j], 1.0f);
+      from_f32(beta.v[i].v[j], 0.0f);
     }
+  if (kKeep) {
+    if (p.gamma != nullptr) take<WT, V>(static_cast<const WT*>(p.gamma), p.H, 0.0f, gamma);
+    if (p.beta != nullptr) take<WT, V>(static_cast<const WT*>(p.beta), p.H, 0.0f, beta);
   }
   __syncthreads();
   int stage = 0;
   uint32_t phase = 0;
   for (long long row = blockIdx.x; row < p.M; row += gridDim.x) {
+    uint8_t* place = norm_smem + stage * stage_bytes;
     mbar_wait_drain(smem_u32(bars + stage), phase);
-    VT xv[NV];
-    const T* in = reinterpret_cast<const T*>(norm_smem + stage * bytes);
-    load_row<T, V>(in, p.H, true, xv);
-    float mean, rstd;
-    row_stats<T, V>(xv, p.H, inv, p.eps, slot, mean, rstd);
-    __syncwarp();
-    if (threadIdx.x == 0) {
-      const long long ahead = row + static_cast<long long>(stages) * gridDim.x;
-      if (ahead < p.M)
-        norm_copy(norm_smem + stage * bytes, x + ahead * p.ldx, bytes, smem_u32(bars + stage), true);
-      if (p.mean != nullptr) p.mean[row] = mean;
-      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    if (V * sizeof(T) < 16 && (row == 0 || row == p.M - 1)) {
+      norm_edges<T>(rows, row, place);
+      __syncthreads();
     }
+    const uint8_t* at = rows.base + row * rows.ld;
+    const T* in = reinterpret_cast<const T*>(place + (at - down16(at)));
+    Pair x[NP];
+    {
+      Held<T, V> held;
+      take<T, V>(in, p.H, 0.0f, held);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) x[k] = pair_at(held, k);
+    }
+    Pair s = x[0];
+#pragma unroll
+    for (int k = 1; k < NP; ++k) s = add2(s, x[k]);
+    const float mean = row_sum(sum(s), slot, 0) * inv;
+    __syncwarp();
+    if (threadIdx.x == 0) ask(stage, row + static_cast<long long>(stages) * gridDim.x);
     if (++stage == stages) {
       stage = 0;
       phase ^= 1u;
     }
-    store_row<T, WT, V>(p, row, xv, mean, rstd);
+    Pair q = both(0.0f);
+    const Pair shift = both(-mean);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      x[k] = add2(x[k], shift);
+      if constexpr (V == 1) {
+        const int c0 = 2 * k * blockDim.x + threadIdx.x;
+        const float2 f = split(x[k]);
+        x[k] = pair(c0 < p.H ? f.x : 0.0f, c0 + static_cast<int>(blockDim.x) < p.H ? f.y : 0.0f);
+      } else {
+        if (static_cast<int>((k / (V / 2) * blockDim.x + threadIdx.x) * V) >= p.H) x[k] = both(0.0f);
+      }
+      q = fma2(x[k], x[k], q);
+    }
+    if (!kKeep) {
+      if (p.gamma != nullptr) take<WT, V>(static_cast<const WT*>(p.gamma), p.H, 0.0f, gamma);
+      if (p.beta != nullptr) take<WT, V>(static_cast<const WT*>(p.beta), p.H, 0.0f, beta);
+    }
+    const float rstd = rsqrtf(row_sum(sum(q), slot, 1) * inv + p.eps);
+    if (threadIdx.x == 0) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+    const Pair scale = both(rstd);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) x[k] = fma2(mul2(x[k], scale), pair_at(gamma, k), pair_at(beta, k));
+    put_pairs<T, V>(static_cast<T*>(p.y) + row * p.ldy, p.H, x);
   }
 }
 
@@ -277,7 +491,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_wide_kernel(const NormLa
     const float d = to_f32(x[c]) - mean;
     d2 += d * d;
   }
-  const float rstd = 1.0f / sqrtf(row_sum2(make_float2(d2, 0.0f), slot, 1).x * inv + p.eps);
+  const float rstd = rsqrtf(row_sum2(make_float2(d2, 0.0f), slot, 1).x * inv + p.eps);
   if (threadIdx.x == 0) {
     if (p.mean != nullptr) p.mean[row] = mean;
     if (p.rstd != nullptr) p.rstd[row] = rstd;
@@ -319,7 +533,7 @@ __device__ __forceinline__ float2 bwd_sums(const Vec<T, V> (&xv)[kEpt / V], cons
       for (int j = 0; j < V; ++j) {
         const float d = to_f32(gv[i].v[j]);
         const float xh = (to_f32(xv[i].v[j]) - mean) * rstd;
-        const float g = d * to_f32(gw[i].v[j]);
+        const float g = __fmul_rn(d, to_f32(gw[i].v[j]));  // the same value below: its mean cancels in a row of one
         s.x += g;
         s.y = fmaf(g, xh, s.y);
         dg[i][j] = fmaf(d, xh, dg[i][j]);
@@ -342,7 +556,7 @@ __device__ __forceinline__ void bwd_store(const NormLaunch& p, long long row, co
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float xh = (to_f32(xv[i].v[j]) - mean) * rstd;
-        from_f32(o.v[j], rstd * (to_f32(gv[i].v[j]) * to_f32(gw[i].v[j]) - c1 - xh * c2));
+        from_f32(o.v[j], rstd * (__fmul_rn(to_f32(gv[i].v[j]), to_f32(gw[i].v[j])) - c1 - xh * c2));
       }
       *reinterpret_cast<Vec<T, V>*>(dx + c) = o;
     }
@@ -414,47 +628,103 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_kernel(const Norm
     flip ^= 1;
     if (on) bwd_store<T, WT, V>(p, row, cur.x, cur.g, gw, cur.mean, cur.rstd, s.x * inv, s.y * inv);
   }
-  if (p.partial != nullptr)
-    bwd_lines<V>(p, static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y,
-                 static_cast<long long>(gridDim.x) * blockDim.y, dg, db);
+  if (p.partial == nullptr) return;
+  if (blockDim.y == 1) {
+    bwd_lines<V>(p, blockIdx.x, gridDim.x, dg, db);
+    return;
+  }
+  // the block's row groups first, in order (H <= 2048 where there are several)
+  __shared__ float sums[2][kShortRow];
+  for (int y = 0; y < static_cast<int>(blockDim.y); ++y) {
+    if (static_cast<int>(threadIdx.y) == y) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * V;
+        if (c < p.H)
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            sums[0][c + j] = y == 0 ? dg[i][j] : sums[0][c + j] + dg[i][j];
+            sums[1][c + j] = y == 0 ? db[i][j] : sums[1][c + j] + db[i][j];
+          }
+      }
+    }
+    __syncthreads();
+  }
+  const int threads = blockDim.x * blockDim.y, t = threadIdx.y * blockDim.x + threadIdx.x;
+  for (int c = t; c < p.H; c += threads) {
+    p.partial[static_cast<long long>(blockIdx.x) * p.H + c] = sums[0][c];
+    p.partial[(static_cast<long long>(gridDim.x) + blockIdx.x) * p.H + c] = sums[1][c];
+  }
 }
 
 // The same through a ring of whole rows (see norm_ring_kernel), x's and dy's.
-template <typename T, typename WT>
-__global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const NormLaunch p, int stages) {
-  constexpr int V = 16 / sizeof(T);
-  constexpr int NV = kEpt / V;
+template <typename T, typename WT, int V>
+__global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const NormLaunch p, int stages,
+                                                                           int stage_bytes) {
+  constexpr int NP = kEpt / 2;
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ float2 slot[2 * 32];
   __shared__ uint64_t bars[kNormStages];
   const float inv = 1.0f / static_cast<float>(p.H);
-  const uint32_t bytes = static_cast<uint32_t>(p.H) * sizeof(T);
-  const T* x = static_cast<const T*>(p.x);
-  const T* dy = static_cast<const T*>(p.dy);
+  const NormRows xs = norm_rows<T>(p.x, p.ldx, p.M, p.H), gs = norm_rows<T>(p.dy, p.ldy, p.M, p.H);
+  const int half = stage_bytes / 2;
   auto ask = [&](int s, long long row) {
     if (row >= p.M) return;
-    norm_copy(norm_smem + 2 * s * bytes, x + row * p.ldx, bytes, smem_u32(bars + s), true, true);
-    norm_copy(norm_smem + (2 * s + 1) * bytes, dy + row * p.ldy, bytes, smem_u32(bars + s), false);
+    const uint32_t bar = smem_u32(bars + s);
+    mbar_arrive_expect_tx(bar, norm_ask_bytes(xs, row) + norm_ask_bytes(gs, row));
+    norm_ask(xs, row, norm_smem + s * stage_bytes, bar);
+    norm_ask(gs, row, norm_smem + s * stage_bytes + half, bar);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(bars + s), 1);
     mbar_fence_init();
     for (int s = 0; s < stages; ++s) ask(s, blockIdx.x + static_cast<long long>(s) * gridDim.x);
   }
-  float dg[NV][V], db[NV][V];
-  Vec<WT, V> gw[NV];
-  bwd_start<WT, V>(p, gw, dg, db);
+  Held<WT, V> gw;
+  Pair dg[NP], db[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) dg[k] = db[k] = both(0.0f);
+#pragma unroll
+  for (int i = 0; i < kEpt / V; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) from_f32(gw.v[i].v[j], 1.0f);
+  if (p.gamma != nullptr) take<WT, V>(static_cast<const WT*>(p.gamma), p.H, 0.0f, gw);
   __syncthreads();
   int stage = 0, flip = 0;
   uint32_t phase = 0;
+  float mean_next = __ldg(p.mean + blockIdx.x), rstd_next = __ldg(p.rstd + blockIdx.x);  // (grid <= M)
   for (long long row = blockIdx.x; row < p.M; row += gridDim.x) {
-    const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
+    const float mean = mean_next, rstd = rstd_next;
+    if (row + gridDim.x < p.M) {
+      mean_next = __ldg(p.mean + row + gridDim.x);
+      rstd_next = __ldg(p.rstd + row + gridDim.x);
+    }
+    uint8_t* place = norm_smem + stage * stage_bytes;
     mbar_wait_drain(smem_u32(bars + stage), phase);
-    Vec<T, V> xv[NV], gv[NV];
-    load_row<T, V>(reinterpret_cast<const T*>(norm_smem + 2 * stage * bytes), p.H, true, xv);
-    load_row<T, V>(reinterpret_cast<const T*>(norm_smem + (2 * stage + 1) * bytes), p.H, true, gv);
-    float2 s = bwd_sums<T, WT, V>(xv, gv, gw, mean, rstd, p.H, dg, db);
-    s = row_sum2(s, slot, flip);
+    if (V * sizeof(T) < 16 && (row == 0 || row == p.M - 1)) {
+      norm_edges<T>(xs, row, place);
+      norm_edges<T>(gs, row, place + half);
+      __syncthreads();
+    }
+    const uint8_t *xa = xs.base + row * xs.ld, *ga = gs.base + row * gs.ld;
+    Pair xh[NP], d[NP];
+    Held<T, V> xv, gv;
+    // past the row dy = 0, which adds nothing to any sum
+    take<T, V>(reinterpret_cast<const T*>(place + (xa - down16(xa))), p.H, 0.0f, xv);
+    take<T, V>(reinterpret_cast<const T*>(place + half + (ga - down16(ga))), p.H, 0.0f, gv);
+    Pair s1 = both(0.0f), s2 = both(0.0f);
+    const Pair shift = both(-mean), scale = both(rstd);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      xh[k] = mul2(add2(pair_at(xv, k), shift), scale);
+      const Pair dy = pair_at(gv, k);
+      dg[k] = fma2(dy, xh[k], dg[k]);
+      db[k] = add2(db[k], dy);
+      d[k] = mul2(dy, pair_at(gw, k));
+      s1 = add2(s1, d[k]);
+      s2 = fma2(d[k], xh[k], s2);
+    }
+    const float2 s = row_sum2(make_float2(sum(s1), sum(s2)), slot, flip);
     flip ^= 1;
     __syncwarp();
     if (threadIdx.x == 0) ask(stage, row + static_cast<long long>(stages) * gridDim.x);
@@ -462,9 +732,17 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const
       stage = 0;
       phase ^= 1u;
     }
-    if (p.dx != nullptr) bwd_store<T, WT, V>(p, row, xv, gv, gw, mean, rstd, s.x * inv, s.y * inv);
+    if (p.dx != nullptr) {
+      const Pair c1 = both(-s.x * inv), c2 = both(-s.y * inv);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) d[k] = mul2(fma2(xh[k], c2, add2(d[k], c1)), scale);
+      put_pairs<T, V>(static_cast<T*>(p.dx) + row * p.lddx, p.H, d);
+    }
   }
-  if (p.partial != nullptr) bwd_lines<V>(p, blockIdx.x, gridDim.x, dg, db);
+  if (p.partial != nullptr) {
+    put_pairs<float, V>(p.partial + static_cast<long long>(blockIdx.x) * p.H, p.H, dg);
+    put_pairs<float, V>(p.partial + (static_cast<long long>(gridDim.x) + blockIdx.x) * p.H, p.H, db);
+  }
 }
 
 // dx of rows too long for the registers: one block a row, two passes.
@@ -478,7 +756,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_wide_kernel(const No
   const float inv = 1.0f / static_cast<float>(p.H);
   float2 s = make_float2(0.0f, 0.0f);
   for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
-    const float g = to_f32(dy[c]) * weight_at(p.gamma, p.w_f32, c, 1.0f);
+    const float g = __fmul_rn(to_f32(dy[c]), weight_at(p.gamma, p.w_f32, c, 1.0f));
     s.x += g;
     s.y += g * ((to_f32(x[c]) - mean) * rstd);
   }
@@ -486,7 +764,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_wide_kernel(const No
   const float c1 = s.x * inv, c2 = s.y * inv;
   T* dx = static_cast<T*>(p.dx) + row * p.lddx;
   for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
-    const float g = to_f32(dy[c]) * weight_at(p.gamma, p.w_f32, c, 1.0f);
+    const float g = __fmul_rn(to_f32(dy[c]), weight_at(p.gamma, p.w_f32, c, 1.0f));
     from_f32(dx[c], rstd * (g - c1 - (to_f32(x[c]) - mean) * rstd * c2));
   }
 }
@@ -554,15 +832,19 @@ int norm_blocks(int M, const dim3& b, int registers) {
   return static_cast<int>(need < cap ? need : cap);
 }
 
-// The ring's stages for a block (0: rows too short or not 16 bytes wide).
-// room: shared memory of a block; rows: rows of a stage.
-int norm_ring_stages(int v, int size, int H, int room, int rows) {
-  if (v * size != 16 || H * size < 2048) return 0;
-  const int n = room / (rows * H * size);
+// Bytes of a row's place in the ring: its 16-byte pieces, wherever it begins.
+int norm_place(int size, int H) { return (H * size + 15) / 16 * 16 + 16; }
+
+// The ring's stages for a block with `room` bytes (0: the rows are too short; a
+// copy costs about as long as 1 KB takes, so short rows go through registers,
+// several to a block). rows: rows of a stage.
+int norm_ring_stages(int size, int H, int room, int rows) {
+  if (H * size < 2048) return 0;
+  const int n = room / (rows * norm_place(size, H));
   return n < kNormStages ? n : kNormStages;
 }
 
-template <void (*kernel)(const NormLaunch, int)>
+template <void (*kernel)(const NormLaunch, int, int)>
 cudaError_t norm_ring_launch(const NormLaunch& L, int grid, int threads, int stages, int rows,
                              cudaStream_t stream) {
   static bool set[64] = {};  // the attribute holds for the process: once per device and kernel
@@ -575,56 +857,64 @@ cudaError_t norm_ring_launch(const NormLaunch& L, int grid, int threads, int sta
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  const size_t smem = static_cast<size_t>(stages) * rows * L.H * (L.x_f32 ? 4 : 2);
-  kernel<<<grid, threads, smem, stream>>>(L, stages);
+  const int stage = rows * norm_place(L.x_f32 ? 4 : 2, L.H);
+  kernel<<<grid, threads, static_cast<size_t>(stages) * stage, stream>>>(L, stages, stage);
   return cudaGetLastError();
 }
 
-template <typename T, typename WT>
+template <typename T, typename WT, int V>
 cudaError_t norm_forward_launch(const NormLaunch& L, cudaStream_t stream) {
   const dim3 b = norm_block(L.H);
-  const int v = norm_vec(L, false);
-  // blocks an SM: at least two for the ring, so that one's sums run under the other's stores
-  const int per_sm = 65536 / (64 * static_cast<int>(b.x)) > 1 ? 65536 / (64 * static_cast<int>(b.x)) : 1;
-  const int ring_blocks = per_sm < 4 ? per_sm : 4;
-  const int stages = norm_ring_stages(v, sizeof(T), L.H, 200 * 1024 / ring_blocks, 1);
+  const bool is_long = b.x > 512;
+  // blocks an SM: as many as the registers allow, so that one's sums run under another's stores
+  const int regs = is_long || kNormSlim<T, WT, V> ? 64 : 128;
+  const int per_sm = 65536 / (regs * static_cast<int>(b.x)) > 1 ? 65536 / (regs * static_cast<int>(b.x)) : 1;
+  const int ring_blocks = per_sm < 8 ? per_sm : 8;
+  const int stages = norm_ring_stages(sizeof(T), L.H, 200 * 1024 / ring_blocks, 1);
   if (stages >= 2) {
     const long long most = static_cast<long long>(device_sm_count()) * ring_blocks;
-    return norm_ring_launch<norm_ring_kernel<T, WT>>(L, static_cast<int>(L.M < most ? L.M : most),
-                            static_cast<int>(b.x), stages, 1, stream);
+    const int grid = static_cast<int>(L.M < most ? L.M : most), threads = static_cast<int>(b.x);
+    return is_long
+               ? norm_ring_launch<norm_ring_kernel<T, WT, V, true>>(L, grid, threads, stages, 1, stream)
+               : norm_ring_launch<norm_ring_kernel<T, WT, V, false>>(L, grid, threads, stages, 1, stream);
   }
-  const unsigned grid = static_cast<unsigned>(norm_blocks(L.M, b, 64));
-  if (v == 16 / static_cast<int>(sizeof(T)))
-    norm_kernel<T, WT, 16 / sizeof(T)><<<grid, b, 0, stream>>>(L);
-  else if (v == 2)
-    norm_kernel<T, WT, 2><<<grid, b, 0, stream>>>(L);
-  else
-    norm_kernel<T, WT, 1><<<grid, b, 0, stream>>>(L);
+  norm_kernel<T, WT, V><<<static_cast<unsigned>(norm_blocks(L.M, b, 64)), b, 0, stream>>>(L);
   return cudaGetLastError();
 }
 
+constexpr int kNormRingBlocks = 4;  // blocks an SM in the backward pass, at most: each leaves a line
+
 // `lines` receives the table's lines.
-template <typename T, typename WT>
+template <typename T, typename WT, int V>
 cudaError_t norm_backward_launch(const NormLaunch& L, int* lines, cudaStream_t stream) {
   const dim3 b = norm_block(L.H);
-  const int v = norm_vec(L, true);
   const int per_sm = 65536 / (128 * static_cast<int>(b.x)) > 1 ? 65536 / (128 * static_cast<int>(b.x)) : 1;
-  const int ring_blocks = per_sm < 2 ? per_sm : 2;
-  const int stages = norm_ring_stages(v, sizeof(T), L.H, 200 * 1024 / ring_blocks, 2);
+  const int ring_blocks = per_sm < kNormRingBlocks ? per_sm : kNormRingBlocks;
+  const int stages = norm_ring_stages(sizeof(T), L.H, 200 * 1024 / ring_blocks, 2);
   if (stages >= 2) {
     const long long most = static_cast<long long>(device_sm_count()) * ring_blocks;
     *lines = static_cast<int>(L.M < most ? L.M : most);
-    return norm_ring_launch<norm_bwd_ring_kernel<T, WT>>(L, *lines, static_cast<int>(b.x), stages, 2, stream);
+    return norm_ring_launch<norm_bwd_ring_kernel<T, WT, V>>(L, *lines, static_cast<int>(b.x), stages, 2, stream);
   }
   const unsigned grid = static_cast<unsigned>(norm_blocks(L.M, b, 128));
-  *lines = static_cast<int>(grid * b.y);
-  if (v == 16 / static_cast<int>(sizeof(T)))
-    norm_bwd_kernel<T, WT, 16 / sizeof(T)><<<grid, b, 0, stream>>>(L);
-  else if (v == 2)
-    norm_bwd_kernel<T, WT, 2><<<grid, b, 0, stream>>>(L);
-  else
-    norm_bwd_kernel<T, WT, 1><<<grid, b, 0, stream>>>(L);
+  *lines = static_cast<int>(grid);
+  norm_bwd_kernel<T, WT, V><<<grid, b, 0, stream>>>(L);
   return cudaGetLastError();
+}
+
+template <typename T, typename WT>
+cudaError_t norm_forward_width(const NormLaunch& L, cudaStream_t stream) {
+  const int v = norm_vec(L, false);
+  return v == 16 / static_cast<int>(sizeof(T)) ? norm_forward_launch<T, WT, 16 / sizeof(T)>(L, stream)
+         : v == 2                              ? norm_forward_launch<T, WT, 2>(L, stream)
+                                               : norm_forward_launch<T, WT, 1>(L, stream);
+}
+template <typename T, typename WT>
+cudaError_t norm_backward_width(const NormLaunch& L, int* lines, cudaStream_t stream) {
+  const int v = norm_vec(L, true);
+  return v == 16 / static_cast<int>(sizeof(T)) ? norm_backward_launch<T, WT, 16 / sizeof(T)>(L, lines, stream)
+         : v == 2                              ? norm_backward_launch<T, WT, 2>(L, lines, stream)
+                                               : norm_backward_launch<T, WT, 1>(L, lines, stream);
 }
 
 template <typename T>
@@ -633,7 +923,7 @@ cudaError_t run_norm(const NormLaunch& L, cudaStream_t stream) {
     norm_wide_kernel<T><<<L.M, kNormMaxThreads, 0, stream>>>(L);
     return cudaGetLastError();
   }
-  return L.w_f32 ? norm_forward_launch<T, float>(L, stream) : norm_forward_launch<T, __nv_bfloat16>(L, stream);
+  return L.w_f32 ? norm_forward_width<T, float>(L, stream) : norm_forward_width<T, __nv_bfloat16>(L, stream);
 }
 
 template <typename T>
@@ -650,18 +940,18 @@ cudaError_t run_norm_backward(const NormLaunch& L, cudaStream_t stream) {
     if (L.dx != nullptr) norm_bwd_wide_kernel<T><<<L.M, kNormMaxThreads, 0, stream>>>(L);
     e = cudaGetLastError();
   } else {
-    e = L.w_f32 ? norm_backward_launch<T, float>(L, &lines, stream)
-                : norm_backward_launch<T, __nv_bfloat16>(L, &lines, stream);
+    e = L.w_f32 ? norm_backward_width<T, float>(L, &lines, stream)
+                : norm_backward_width<T, __nv_bfloat16>(L, &lines, stream);
   }
   if (e != cudaSuccess || L.partial == nullptr) return e;
   return launch_sum_lines(L.partial, 2, lines, L.H, L.dgamma, L.dbeta, stream);
 }
 
-// A table's lines added up (weight and bias gradients): 8 warps take every eighth
-// line of 32 columns, then one warp adds the eight sums in order.
-__global__ void __launch_bounds__(256) sum_lines_kernel(const float* partial, int lines, int H,
+// A table's lines added up (weight and bias gradients): 32 warps take every 32nd
+// line of 32 columns, then one warp adds the 32 sums in order.
+__global__ void __launch_bounds__(1024) sum_lines_kernel(const float* partial, int lines, int H,
                                                         float* out0, float* out1) {
-  __shared__ float sum[8][33];
+  __shared__ float sum[32][33];
   float* out = blockIdx.y == 0 ? out0 : out1;
   if (out == nullptr) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -670,11 +960,11 @@ __global__ void __launch_bounds__(256) sum_lines_kernel(const float* partial, in
   float s = 0.0f;
   if (c < H)
 #pragma unroll 8
-    for (int l = w; l < lines; l += 8) s += src[static_cast<long long>(l) * H];
+    for (int l = w; l < lines; l += 32) s += src[static_cast<long long>(l) * H];
   sum[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < H) {
-    for (int i = 1; i < 8; ++i) s += sum[i][lane];
+    for (int i = 1; i < 32; ++i) s += sum[i][lane];
     out[c] = s;
   }
 }
@@ -684,15 +974,14 @@ __global__ void __launch_bounds__(256) sum_lines_kernel(const float* partial, in
 cudaError_t launch_sum_lines(const float* table, int tables, int lines, int H, float* out0,
                              float* out1, cudaStream_t stream) {
   const dim3 grid((static_cast<unsigned>(H) + 31) / 32, static_cast<unsigned>(tables));
-  sum_lines_kernel<<<grid, 256, 0, stream>>>(table, lines, H, out0, out1);
+  sum_lines_kernel<<<grid, 1024, 0, stream>>>(table, lines, H, out0, out1);
   return cudaGetLastError();
 }
 
 int norm_partial_rows(int M, int H) {
   if (norm_bwd_wide(H)) return M < 32 ? M : 32;
-  const dim3 b = norm_block(H);
-  const int lines = norm_blocks(M, b, 128) * static_cast<int>(b.y);
-  const long long ring = 2ll * device_sm_count();  // the ring's blocks, at most
+  const int lines = norm_blocks(M, norm_block(H), 128);
+  const long long ring = static_cast<long long>(kNormRingBlocks) * device_sm_count();
   const int most = static_cast<int>(M < ring ? M : ring);
   return lines > most ? lines : most;
 }
