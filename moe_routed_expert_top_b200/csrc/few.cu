@@ -617,6 +617,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(const FewParam
     const int rows = row0 + (row1 - row0) * (pass + 1) / passes - rb;
     for (int i = lane; i < TP * kPitch; i += 32) mine[i] = 0.0f;
     __syncwarp();
+    // the residual of the thread's first output: asked for now, its way from memory is
+    // as long as a small layer's items
+    float res0 = 0.0f;
+    {
+      const int t = threadIdx.x / kRows, row = threadIdx.x % kRows;
+      if (p.residual != nullptr && t < p.T && row < rows)
+        res0 = __bfloat162float(p.residual[static_cast<int64_t>(t) * p.H + rb + row]);
+    }
     // weights of an item: kSpan 1: block m = rows 16m..; kSpan 2: block m = k 64m..
     auto load = [&](FewA& a, uint4 (&b)[2 * kSpan], const DownWalk& d) {
       const bool on = d.left > 0;
@@ -722,7 +730,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(const FewParam
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) s += table[(w * TP + t) * kPitch + row];
         const int64_t at = static_cast<int64_t>(t) * p.H + rb + row;
-        if (p.residual != nullptr) s += __bfloat162float(p.residual[at]);
+        if (i == static_cast<int>(threadIdx.x))
+          s += res0;
+        else if (p.residual != nullptr)
+          s += __bfloat162float(p.residual[at]);
         p.out[at] = __float2bfloat16(s);
       }
     }
