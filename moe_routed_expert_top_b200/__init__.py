@@ -28,7 +28,7 @@ __all__ = [
     "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward", "EXPORTED_SYMBOLS",
     "MOE_OK", "MOE_EPI_STORE", "MOE_EPI_SWIGLU", "MOE_EPI_SWIGLU_FP8", "MOE_EPI_STORE_F32",
     "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_DEV_BAD_EXPERT_ID", "MOE_DEV_TIMEOUT",
-    "MOE_FEW_MAX_TOKENS", "MOE_ACT_NONE", "MOE_ACT_RELU", "MOE_ACT_SILU", "MOE_ACT_GELU",
+    "MOE_FEW_MAX_TOKENS", "MOE_LINEAR_FEW_ROWS", "MOE_ACT_NONE", "MOE_ACT_RELU", "MOE_ACT_SILU", "MOE_ACT_GELU",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -46,6 +46,7 @@ MOE_TILE_WEIGHT_ROWS_PAIR = 0x30
 MOE_A_GATHER = 0x100  # moe_grouped_gemm: A = hidden states, rows gathered through the tables
 MOE_TRANS_PER_BLOCK, MOE_TRANS_PER_TILE = 0, 1
 MOE_FEW_MAX_TOKENS = 64
+MOE_LINEAR_FEW_ROWS = 16
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU = 0, 1, 2, 3
 
 EXPORTED_SYMBOLS = (
@@ -410,9 +411,9 @@ def moe_linear_workspace_bytes(desc: LinearDesc) -> int:
     return int(lib().moe_linear_workspace_bytes(ctypes.byref(desc)))
 
 
-def moe_linear(desc, x, w, bias, residual, y, z, workspace, ws_bytes=None, stream=None):
+def moe_linear(desc, x, w, bias, residual, y, z, workspace=None, ws_bytes=None, stream=None):
     if ws_bytes is None:
-        ws_bytes = workspace.numel() * workspace.element_size()
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     status = lib().moe_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
                               _ptr(y), _ptr(z), _ptr(workspace), ws_bytes, _stream(stream))
     if status:

@@ -223,14 +223,21 @@ moe_status check_linear(const moe_linear_desc* d, LinearShape* out) {
   return MOE_OK;
 }
 
+// The forward pass's product: its sizes, and which operand is which.
+moe::LinearProduct linear_forward_product(const LinearShape& d) {
+  moe::LinearProduct g;
+  g.swap = d.M > moe::kLinearFewRows && d.M <= moe::kLinearSwapRows;
+  g.M = g.swap ? d.N : d.M;
+  g.N = g.swap ? d.M : d.N;
+  g.K = d.K;
+  g.e.y_f32 = d.y_f32;
+  return g;
+}
+
 int64_t linear_forward_bytes(const LinearShape& d) {
   if (d.M <= moe::kLinearFewRows) return 1024;
   if (d.N == 0) return 1024;
-  moe::LinearProduct g;
-  g.M = d.M;
-  g.N = d.N;
-  g.K = d.K;
-  g.e.y_f32 = d.y_f32;
+  const moe::LinearProduct g = linear_forward_product(d);
   return 1024 + 4 * moe::linear_gemm_partial(&g, 1);
 }
 
@@ -1014,23 +1021,22 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
   moe_status s = check_linear(desc, &d);
   if (s != MOE_OK) return s;
   if (d.M == 0 || d.N == 0) return MOE_OK;
-  if (x == nullptr || w == nullptr || y == nullptr || workspace == nullptr)
+  const bool few = d.M <= moe::kLinearFewRows;
+  if (x == nullptr || w == nullptr || y == nullptr || (workspace == nullptr && !few))
     return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(workspace, 32) ||
       !aligned(bias, desc->bias_f32 ? 4 : 2) || !aligned(residual, desc->res_f32 ? 4 : 2) ||
       !aligned(y, desc->y_f32 ? 4 : 2) || !aligned(z, 2))
     return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < static_cast<size_t>(linear_forward_bytes(d))) return MOE_ERR_WORKSPACE;
+  if (workspace != nullptr && ws_bytes < static_cast<size_t>(linear_forward_bytes(d)))
+    return MOE_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  moe::LinearProduct g;
-  g.M = d.M;
-  g.N = d.N;
-  g.K = d.K;
-  g.A = x;
-  g.B = w;
-  g.lda = d.ldx;
-  g.ldb = d.ldw;
+  moe::LinearProduct g = linear_forward_product(d);
+  g.A = g.swap ? w : x;
+  g.B = g.swap ? x : w;
+  g.lda = g.swap ? d.ldw : d.ldx;
+  g.ldb = g.swap ? d.ldx : d.ldw;
   g.e.act = desc->act;
   g.e.bias_f32 = desc->bias_f32;
   g.e.res_f32 = desc->res_f32;
@@ -1043,7 +1049,7 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
   g.e.ldy = d.ldy;
   g.e.ldz = d.ldz;
   int32_t* status = reinterpret_cast<int32_t*>(base);
-  if (d.M <= moe::kLinearFewRows) {
+  if (few) {
     MOE_CUDA_TRY(moe::launch_linear_few(g, status, st));
     return MOE_OK;
   }

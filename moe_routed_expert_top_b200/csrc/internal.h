@@ -204,13 +204,20 @@ struct LinearEpilogue {
 struct LinearProduct {
   int M = 0, N = 0, K = 0;
   int a_mn = 0, b_mn = 0;
+  int swap = 0;  // C^T: the epilogue's rows are C's columns
   const void* A = nullptr;
   const void* B = nullptr;
   long long lda = 0, ldb = 0;  // row pitches, elements
   LinearEpilogue e;
 };
-// Rows of x up to which the weight-streaming kernel runs instead of the tiles.
-constexpr int kLinearFewRows = 64;
+// Rows of x up to which the weight streams through registers (linear_few.cu). Measured
+// against the tiles, 16384 x 7168: 40 us at 8 rows and 65 at 16 against 53 (and more as
+// the rows' words come from L1 for each weight row); 256 x 7168: 5 to 8 us against 11.
+constexpr int kLinearFewRows = 16;
+// Up to so many rows the tiles' rows are the weight's: 256 rows of the weight meet 32 to
+// 128 rows of x, where a tile of 256 rows of x would be mostly empty and its ring
+// hold fewer of the weight's bytes.
+constexpr int kLinearSwapRows = 128;
 cudaError_t launch_linear_few(const LinearProduct& L, int32_t* status, cudaStream_t stream);
 // One or two products in one launch (count 1 or 2); partial: linear_gemm_partial()
 // floats (which goes by the products' sizes and y_f32), 32-byte aligned.

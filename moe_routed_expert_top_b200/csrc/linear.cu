@@ -69,11 +69,12 @@ struct LinProblem {
   int M, N;
   int a_mn, b_mn;
   int a_3d, b_3d;          // the operand's stage is one copy (3-D tensor map)
+  int swap;                // the tile's rows are y's columns (few rows of x: see lin_swapped)
   int bn;                  // tile width: a multiple of 32, at most kMaxBn
   int tiles_m, tiles_n;
   int splits;              // parts of each tile, along k
   int kb_total, kb_split;  // k blocks of 128: all, and of one part
-  float* partial;          // [splits][tiles][256][bn] sums of the parts
+  float* partial;          // [splits][tiles][256][bn] sums of the parts (swap: [bn][256])
   int wide;                // every row of y, z and residual takes 32-byte accesses
   LinearEpilogue e;
 };
@@ -430,9 +431,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       const int c0 = it.tn * p.bn;
       const int width = min(p.bn, p.N - c0);
       const bool has_bias = !sums && p.e.bias != nullptr;
-      const bool fetch = !sums && p.wide && p.e.res != nullptr && !p.e.res_f32;
+      const bool fetch = !p.swap && !sums && p.wide && p.e.res != nullptr && !p.e.res_f32;
       __syncwarp();
-      if (has_bias)
+      if (has_bias && !p.swap)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = (2 * i + grp) * 32 + lane;
@@ -454,7 +455,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         tmem_ld_wait();
         const int cols = min(32, width - j);
         const float* b = bias + (j >> 6) * 32;
-        if (sums) {
+        if (p.swap) {
+          // the thread's row is a column of y: the lanes lie along y's rows as they are
+          if (lane < rows) {
+            if (sums) {
+              float* dst = it.partial + j * 256 + r0 + lane;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < cols) dst[i * 256] = __uint_as_float(v[i]);
+            } else {
+              const int ny = static_cast<int>(m0) + lane;
+              const float bv = linear_bias(p.e, ny);
+#pragma unroll
+              for (int i0 = 0; i0 < 32; i0 += 8) {
+                float r8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  r8[i] = p.e.res != nullptr && i0 + i < cols ? linear_res(p.e, n + i0 + i, ny) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (i0 + i < cols) {
+                    float z;
+                    const float y = linear_result(p.e, __uint_as_float(v[i0 + i]), bv, r8[i], &z);
+                    linear_put(p.e, n + i0 + i, ny, y, z);
+                  }
+              }
+            }
+          }
+        } else if (sums) {
           if (lane < rows) lin_store32_f32(it.partial + (r0 + lane) * p.bn + j, v);
         } else if (p.wide && cols == 32) {
           uint32_t now[16];
@@ -526,14 +554,17 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
   const int tile = first + blockIdx.y;
   int tm, tn;
   lin_tile(p, tile, tm, tn);
-  const int c = threadIdx.x * 8, n = tn * p.bn + c;
+  // y's rows and columns of the tile, its pitch in the table and where it begins
+  const int height = p.swap ? p.bn : 256, pitch = p.swap ? 256 : p.bn;
+  const int M = p.swap ? p.N : p.M, N = p.swap ? p.M : p.N;
+  const int c = threadIdx.x * 8, n = (p.swap ? tm * 256 : tn * p.bn) + c;
   const int row = blockIdx.x * 8 + threadIdx.y;
-  const long long m = static_cast<long long>(tm) * 256 + row;
+  const long long m = (p.swap ? static_cast<long long>(tn) * p.bn : static_cast<long long>(tm) * 256) + row;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c >= p.bn || n >= p.N || m >= p.M) return;
+  if (c >= pitch || row >= height || n >= N || m >= M) return;
   const long long step = static_cast<long long>(p.tiles_m) * p.tiles_n * 256 * p.bn;
-  const float* src = p.partial + (static_cast<long long>(tile) * 256 + row) * p.bn + c;
-  const int cols = min(8, p.N - n);
+  const float* src = p.partial + static_cast<long long>(tile) * 256 * p.bn + row * pitch + c;
+  const int cols = min(8, N - n);
   const bool fast = p.wide && cols == 8 && !p.e.y_f32 && (p.e.res == nullptr || !p.e.res_f32);
   float bias[8];
 #pragma unroll
@@ -816,6 +847,7 @@ cudaError_t launch_linear_gemm(const LinearProduct* L, int count, float* partial
     p.N = L[i].N;
     p.a_mn = L[i].a_mn;
     p.b_mn = L[i].b_mn;
+    p.swap = L[i].swap;
     p.bn = plan[i].bn;
     p.tiles_m = plan[i].tiles_m;
     p.tiles_n = plan[i].tiles_n;
@@ -862,7 +894,8 @@ cudaError_t launch_linear_gemm(const LinearProduct* L, int count, float* partial
     const int tiles = p.tiles_m * p.tiles_n;
     for (int first = 0; first < tiles && e == cudaSuccess; first += 65535) {  // (grid.y's limit)
       const int n = tiles - first < 65535 ? tiles - first : 65535;
-      cfg.gridDim = dim3(p.M < 256 ? (static_cast<unsigned>(p.M) + 7) / 8 : 32, static_cast<unsigned>(n));
+      const int high = p.swap ? (p.N < p.bn ? p.N : p.bn) : (p.M < 256 ? p.M : 256);  // y's rows of a tile
+      cfg.gridDim = dim3(static_cast<unsigned>(high + 7) / 8, static_cast<unsigned>(n));
       cfg.blockDim = dim3(32, 8);
       cfg.dynamicSmemBytes = 0;
       e = cudaLaunchKernelEx(&cfg, linear_join_kernel, p, first);

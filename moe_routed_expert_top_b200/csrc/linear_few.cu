@@ -1,4 +1,4 @@
-// linear_few.cu - the linear product y = act(x W^T + bias) + residual for a few
+// linear_few.cu - the linear product y = act(x W^T + bias) + residual for 1..16
 // rows of x (a decode step's projections and router logits).
 //
 // What bounds it: the weight's N*K values, read once from HBM. The layout is the
@@ -25,7 +25,7 @@ namespace {
 
 struct LinearFewParams {
   int M, N, K;
-  int tiles, groups;  // row tiles; groups of NT * 8 rows of x
+  int tiles;  // of the weight's rows
   long long ldx, ldw;
   const __nv_bfloat16* x;
   const __nv_bfloat16* w;
@@ -57,16 +57,12 @@ __device__ __forceinline__ void linear_ldw(FewW& v, const __nv_bfloat16* row, in
 
 struct LinearTile {
   int row0, rows;  // rows 0: no tile
-  int t0, n;       // rows of x
 };
 
-__device__ __forceinline__ LinearTile linear_tile(const LinearFewParams& p, int per, int i) {
+__device__ __forceinline__ LinearTile linear_tile(const LinearFewParams& p, int i) {
   LinearTile t;
-  const int c = i % p.tiles, gr = i / p.tiles;
-  t.row0 = static_cast<int>(static_cast<int64_t>(p.N) * c / p.tiles);
-  t.rows = gr < p.groups ? static_cast<int>(static_cast<int64_t>(p.N) * (c + 1) / p.tiles) - t.row0 : 0;
-  t.t0 = gr * per;
-  t.n = min(per, p.M - t.t0);
+  t.row0 = static_cast<int>(static_cast<int64_t>(p.N) * i / p.tiles);
+  t.rows = i < p.tiles ? static_cast<int>(static_cast<int64_t>(p.N) * (i + 1) / p.tiles) - t.row0 : 0;
   return t;
 }
 
@@ -78,15 +74,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_few_kernel(const Linear
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
   const int rounds = (p.K + kFewWarps * kWide * kDepth - 1) / (kFewWarps * kWide * kDepth);
-  // a weight that several groups read stays in L2
-  const uint64_t policy = p.groups > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing here waits on a barrier in memory
+  const uint64_t policy = l2_policy_evict_first();
+  // nothing here waits on a barrier in memory
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.status != nullptr) *p.status = 0;
 
   FewA aw[kDepth];
-  uint4 bx[kDepth][2 * kSpan];
+  uint4 bx[kDepth][NT][2 * kSpan];
   // where piece (m, half) of a step lies: its row (kSpan 1: four rows 8 apart, 2: two
   // rows, 4: one) and its chunk of k
-  auto load = [&](FewA& a, uint4 (&b)[2 * kSpan], const LinearTile& t, int step) {
+  auto load = [&](FewA& a, uint4 (&b)[NT][2 * kSpan], const LinearTile& t, int step) {
     const int k0 = (step * kFewWarps + warp) * kWide + q * 16;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -98,20 +94,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_few_kernel(const Linear
                            row < t.rows, policy);
       }
 #pragma unroll
-    for (int i = 0; i < 2 * kSpan; ++i) {
-      const int k = k0 + 64 * (i >> 1) + 8 * (i & 1);
-      b[i] = few_ldx(p.x + static_cast<int64_t>(t.t0 + g) * p.ldx + k, t.rows > 0 && g < t.n && k < p.K);
-    }
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 2 * kSpan; ++i) {
+        const int k = k0 + 64 * (i >> 1) + 8 * (i & 1);
+        b[j][i] = few_ldx(p.x + static_cast<int64_t>(j * 8 + g) * p.ldx + k, t.rows > 0 && j * 8 + g < p.M && k < p.K);
+      }
   };
 
   int tile = blockIdx.x;
-  LinearTile cur = linear_tile(p, NT * 8, tile);
+  LinearTile cur = linear_tile(p, tile);
 #pragma unroll
   for (int d = 0; d < kDepth; ++d) load(aw[d], bx[d], cur, d);
   int flip = 0;
   while (cur.rows > 0) {
     tile += gridDim.x;
-    const LinearTile next = linear_tile(p, NT * 8, tile);
+    const LinearTile next = linear_tile(p, tile);
     float acc[NT][2][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -128,13 +126,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_few_kernel(const Linear
         if (k0 < p.K) {
 #pragma unroll
           for (int j = 0; j < NT; ++j)
-            if (j * 8 < cur.n) {
-              const __nv_bfloat16* xr = p.x + static_cast<int64_t>(cur.t0 + j * 8 + g) * p.ldx;
+            if (j * 8 < p.M) {
 #pragma unroll
               for (int i = 0; i < 2 * kSpan; ++i) {
                 const int z = i >> 1, s = i & 1;
-                const int k = k0 + q * 16 + 64 * z + 8 * s;
-                const uint4 b = j == 0 ? bx[d][i] : few_ldx(xr + k, j * 8 + g < cur.n && k < p.K);
+                const uint4 b = bx[d][j][i];
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                   if (kSpan == 2 && m != z) continue;
@@ -157,7 +153,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_few_kernel(const Linear
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      if (j * 8 < cur.n) {
+      if (j * 8 < p.M) {
         float4(*buf)[kBlocks][32] = red[flip];
         flip ^= 1;
         if (kSpan == 1) {
@@ -174,12 +170,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_few_kernel(const Linear
         const float* rf = reinterpret_cast<const float*>(&buf[0][0][0]);
         const int i = threadIdx.x;
         const int row = i % (16 * kBlocks), col = i / (16 * kBlocks);
-        if (col < 8 && row < cur.rows && j * 8 + col < cur.n) {
+        if (col < 8 && row < cur.rows && j * 8 + col < p.M) {
           const int at = (row >> 4) * 128 + ((row & 7) * 4 + (col >> 1)) * 4 + ((row >> 3) & 1) * 2 + (col & 1);
           float s = 0.0f;
 #pragma unroll
           for (int w = 0; w < kFewWarps; ++w) s += rf[w * kBlocks * 128 + at];
-          linear_store(p.e, cur.t0 + j * 8 + col, cur.row0 + row, s);
+          linear_store(p.e, j * 8 + col, cur.row0 + row, s);
         }
       }
     cur = next;
@@ -199,20 +195,18 @@ cudaError_t run(const LinearFewParams& p, int grid, cudaStream_t stream) {
 template <int NT>
 cudaError_t run_few(LinearFewParams p, cudaStream_t stream) {
   const int sms = device_sm_count();
-  p.groups = (p.M + NT * 8 - 1) / (NT * 8);
   // as many tiles a CTA as tiles of at most 32 rows need, and then rows that make
   // these tiles equal
-  const long long rows_all = static_cast<long long>(p.N) * p.groups;
-  const long long turns = (rows_all + 32ll * sms - 1) / (32ll * sms);
-  long long rows = (rows_all + sms * turns - 1) / (sms * turns);
+  const long long turns = (p.N + 32ll * sms - 1) / (32ll * sms);
+  long long rows = (p.N + sms * turns - 1) / (sms * turns);
   if (rows > 32) rows = 32;
   p.tiles = static_cast<int>((p.N + rows - 1) / rows);
-  const long long all = static_cast<long long>(p.tiles) * p.groups;
-  const int grid = static_cast<int>(all < sms ? all : sms);
+  const int grid = p.tiles < sms ? p.tiles : sms;
   const int most = (p.N + p.tiles - 1) / p.tiles;
-  if (most <= 8) return run<NT, 4, NT == 4 ? 2 : 3>(p, grid, stream);
-  if (most <= 16) return run<NT, 2, NT == 4 ? 3 : 4>(p, grid, stream);
-  return run<NT, 1, NT == 4 ? 3 : 4>(p, grid, stream);
+  // (steps in flight: what 255 registers a thread hold)
+  if (most <= 8) return run<NT, 4, NT == 1 ? 3 : 2>(p, grid, stream);
+  if (most <= 16) return run<NT, 2, NT == 1 ? 4 : 3>(p, grid, stream);
+  return run<NT, 1, NT == 1 ? 4 : 3>(p, grid, stream);
 }
 
 }  // namespace
@@ -228,9 +222,7 @@ cudaError_t launch_linear_few(const LinearProduct& L, int32_t* status, cudaStrea
   p.w = static_cast<const __nv_bfloat16*>(L.B);
   p.e = L.e;
   p.status = status;
-  if (p.M <= 8) return run_few<1>(p, stream);
-  if (p.M <= 16) return run_few<2>(p, stream);
-  return run_few<4>(p, stream);
+  return p.M <= 8 ? run_few<1>(p, stream) : run_few<2>(p, stream);
 }
 
 }  // namespace moe

@@ -16,7 +16,7 @@ import contextlib
 
 import torch
 
-from . import (MOE_FEW_MAX_TOKENS, make_linear_desc, make_problem, moe_experts_forward,
+from . import (MOE_FEW_MAX_TOKENS, MOE_LINEAR_FEW_ROWS, make_linear_desc, make_problem, moe_experts_forward,
                moe_experts_forward_few, moe_few_workspace_bytes, moe_layer_norm,
                moe_layer_norm_backward, moe_layer_norm_backward_workspace_bytes, moe_linear,
                moe_linear_backward, moe_linear_backward_workspace_bytes,
@@ -367,7 +367,10 @@ class Linear:
             if out is None:
                 out = torch.empty(M, self.N, dtype=self.out_dtype, device=dev)
             z = torch.empty(M, self.N, dtype=torch.bfloat16, device=dev) if with_z else None
-            self._ws = ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = None  # a few rows need none
+            if M > MOE_LINEAR_FEW_ROWS:
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            self._ws = ws
             moe_linear(d, x, self.weight, self.bias, residual, out, z, ws, need, _stream_of(x))
         return (out, z) if with_z else out
 
@@ -398,6 +401,8 @@ class Linear:
 
     def device_status(self) -> int:
         """The device status word of the last call (synchronises)."""
+        if self._ws is None:
+            return 0
         return int(self._ws[:4].view(torch.int32).item())
 
 

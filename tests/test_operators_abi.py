@@ -64,12 +64,12 @@ def test_linear_refusals(M):
                            (dict(ldw=65), -2), (dict(ldy=15), -1), (dict(ldz=15), -1), (dict(ldr=15), -1),
                            (dict(ldx=-64), -1), (dict(M=(1 << 24) + 1), -2), (dict(K=1 << 25), -2),
                            (dict(ldx=1 << 40), -2), (dict(x=40), -1), (dict(w=40), -1), (dict(ws=16), -1),
-                           (dict(ws=None), -1), (dict(z=33), -1)):
+                           (dict(M=65, ws=None), -1), (dict(z=33), -1)):
             assert f(M, **kw) == status, (f.__name__, kw)
     for kw in (dict(x=None), dict(w=None), dict(y=None), dict(b=33), dict(b=34, bias_f32=True), dict(r=33),
                dict(r=34, res_f32=True), dict(y=33), dict(y=34, y_f32=True)):
         assert linear(M, **kw) == -1, kw
-    for kw in (dict(dy=None), dict(x=None), dict(w=None), dict(act="silu"), dict(dy=33), dict(dy=34, y_f32=True),
+    for kw in (dict(dy=None), dict(x=None), dict(w=None), dict(ws=None), dict(act="silu"), dict(dy=33), dict(dy=34, y_f32=True),
                dict(dx=40), dict(dw=40), dict(db=34)):
         assert linear_bwd(M, **kw) == -1, kw
     d = M.make_linear_desc(M=4, N=16, K=64)
