@@ -226,7 +226,7 @@ moe_status check_linear(const moe_linear_desc* d, LinearShape* out) {
 // The forward pass's product: its sizes, and which operand is which.
 moe::LinearProduct linear_forward_product(const LinearShape& d) {
   moe::LinearProduct g;
-  g.swap = d.M > moe::kLinearFewRows && d.M <= moe::kLinearSwapRows;
+  g.swap = d.M <= moe::kLinearSwapRows;
   g.M = g.swap ? d.N : d.M;
   g.N = g.swap ? d.M : d.N;
   g.K = d.K;
@@ -235,7 +235,7 @@ moe::LinearProduct linear_forward_product(const LinearShape& d) {
 }
 
 int64_t linear_forward_bytes(const LinearShape& d) {
-  if (d.M <= moe::kLinearFewRows) return 1024;
+  if (moe::linear_is_few(d.M, d.N, d.K)) return 1024;
   if (d.N == 0) return 1024;
   const moe::LinearProduct g = linear_forward_product(d);
   return 1024 + 4 * moe::linear_gemm_partial(&g, 1);
@@ -1021,8 +1021,9 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
   moe_status s = check_linear(desc, &d);
   if (s != MOE_OK) return s;
   if (d.M == 0 || d.N == 0) return MOE_OK;
-  const bool few = d.M <= moe::kLinearFewRows;
-  if (x == nullptr || w == nullptr || y == nullptr || (workspace == nullptr && !few))
+  const bool few = moe::linear_is_few(d.M, d.N, d.K);
+  if (x == nullptr || w == nullptr || y == nullptr ||
+      (workspace == nullptr && d.M > moe::kLinearFewRows))
     return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(workspace, 32) ||
       !aligned(bias, desc->bias_f32 ? 4 : 2) || !aligned(residual, desc->res_f32 ? 4 : 2) ||
@@ -1032,7 +1033,14 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
     return MOE_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  moe::LinearProduct g = linear_forward_product(d);
+  moe::LinearProduct g;
+  if (few) {
+    g.M = d.M;
+    g.N = d.N;
+    g.K = d.K;
+  } else {
+    g = linear_forward_product(d);
+  }
   g.A = g.swap ? w : x;
   g.B = g.swap ? x : w;
   g.lda = g.swap ? d.ldw : d.ldx;

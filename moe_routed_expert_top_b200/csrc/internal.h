@@ -210,10 +210,16 @@ struct LinearProduct {
   long long lda = 0, ldb = 0;  // row pitches, elements
   LinearEpilogue e;
 };
-// Rows of x up to which the weight streams through registers (linear_few.cu). Measured
-// against the tiles, 16384 x 7168: 40 us at 8 rows and 65 at 16 against 53 (and more as
-// the rows' words come from L1 for each weight row); 256 x 7168: 5 to 8 us against 11.
+// Whether the weight streams through registers (linear_few.cu) or through the tiles
+// (linear.cu). The rows' words come from L1 for each tile of weight rows, so the
+// streaming kernel slows with the rows; the tiles cost more to begin and, with few
+// of them, a second kernel. Measured, streaming against tiles: 16384 x 7168 at 8 rows
+// 40 us, 16 rows 51 against 53, 17 rows 62 against 46, 32 rows 69 against 48; 4608 x 2048
+// at 17 rows 8 us against 12; 4096 x 4096 at 17 and 32 rows 13 and 14 against 13 and 14.5.
 constexpr int kLinearFewRows = 16;
+inline bool linear_is_few(int M, int N, int K) {
+  return M <= kLinearFewRows || (M <= 32 && static_cast<long long>(N) * K <= (1ll << 24));
+}
 // Up to so many rows the tiles' rows are the weight's: 256 rows of the weight meet 32 to
 // 128 rows of x, where a tile of 256 rows of x would be mostly empty and its ring
 // hold fewer of the weight's bytes.

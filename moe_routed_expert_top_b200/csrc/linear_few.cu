@@ -1,4 +1,4 @@
-// linear_few.cu - the linear product y = act(x W^T + bias) + residual for 1..16
+// linear_few.cu - the linear product y = act(x W^T + bias) + residual for 1..32
 // rows of x (a decode step's projections and router logits).
 //
 // What bounds it: the weight's N*K values, read once from HBM. The layout is the
@@ -204,9 +204,9 @@ cudaError_t run_few(LinearFewParams p, cudaStream_t stream) {
   const int grid = p.tiles < sms ? p.tiles : sms;
   const int most = (p.N + p.tiles - 1) / p.tiles;
   // (steps in flight: what 255 registers a thread hold)
-  if (most <= 8) return run<NT, 4, NT == 1 ? 3 : 2>(p, grid, stream);
-  if (most <= 16) return run<NT, 2, NT == 1 ? 4 : 3>(p, grid, stream);
-  return run<NT, 1, NT == 1 ? 4 : 3>(p, grid, stream);
+  if (most <= 8) return run<NT, 4, NT == 1 ? 3 : NT == 2 ? 2 : 1>(p, grid, stream);
+  if (most <= 16) return run<NT, 2, NT == 1 ? 4 : NT == 2 ? 3 : 2>(p, grid, stream);
+  return run<NT, 1, NT == 1 ? 4 : NT == 2 ? 3 : 2>(p, grid, stream);
 }
 
 }  // namespace
@@ -222,7 +222,7 @@ cudaError_t launch_linear_few(const LinearProduct& L, int32_t* status, cudaStrea
   p.w = static_cast<const __nv_bfloat16*>(L.B);
   p.e = L.e;
   p.status = status;
-  return p.M <= 8 ? run_few<1>(p, stream) : run_few<2>(p, stream);
+  return p.M <= 8 ? run_few<1>(p, stream) : p.M <= 16 ? run_few<2>(p, stream) : run_few<4>(p, stream);
 }
 
 }  // namespace moe
