@@ -518,8 +518,9 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
  * (dense; each may be NULL and is then not computed). The residual's gradient is
  * dy itself. dy [M, N] has y's type and pitch (ldy); z (bf16, pitch ldz) is
  * moe_linear's z, needed unless act is MOE_ACT_NONE. dz is an operand of two
- * bf16 matrix products, so there it is rounded to bf16 once; dbias sums it
- * unrounded. Sums are fp32, in a fixed order. M == 0 writes zeros into dw and dbias.
+ * bf16 matrix products, so there it is rounded to bf16 once (not up to 64 rows and
+ * 64 columns, which one fp32 kernel does); dbias sums it unrounded. Sums are fp32,
+ * in a fixed order. M == 0 writes zeros into dw and dbias.
  * Arguments and errors as moe_linear; the descriptor's bias_f32, res_f32 and ldr are
  * not used, x may be NULL without dw and w without dx. */
 size_t moe_linear_backward_workspace_bytes(const moe_linear_desc* desc);

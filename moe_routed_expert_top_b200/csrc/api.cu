@@ -1100,6 +1100,28 @@ moe_status moe_linear_backward(const moe_linear_desc* desc, const void* dy, cons
   const LinearBackwardPlan b = plan_linear_backward(d);
   if (ws_bytes < static_cast<size_t>(b.total)) return MOE_ERR_WORKSPACE;
   uint8_t* base = static_cast<uint8_t*>(workspace);
+  if (d.M <= moe::kLinearSmall && d.N <= moe::kLinearSmall) {
+    moe::LinearSmallLaunch q;
+    q.e.M = d.M;
+    q.e.N = d.N;
+    q.e.act = desc->act;
+    q.e.dy_f32 = desc->y_f32;
+    q.e.dy = dy;
+    q.e.z = desc->act != MOE_ACT_NONE ? z : nullptr;
+    q.e.lddy = d.ldy;
+    q.e.ldz = d.ldz;
+    q.e.dbias = dbias;
+    q.K = d.K;
+    q.x = x;
+    q.w = w;
+    q.ldx = d.ldx;
+    q.ldw = d.ldw;
+    q.dx = dx;
+    q.dw = dw;
+    q.status = reinterpret_cast<int32_t*>(base);
+    MOE_CUDA_TRY(moe::launch_linear_small_backward(q, st));
+    return MOE_OK;
+  }
   // the products take dy itself where it is already their operand
   const bool direct = desc->act == MOE_ACT_NONE && !desc->y_f32 && d.ldy % 8 == 0 && aligned(dy, 16);
   const bool products = dx != nullptr || dw != nullptr;

@@ -243,6 +243,20 @@ struct LinearDzLaunch {
 };
 cudaError_t launch_linear_dz(const LinearDzLaunch& L, cudaStream_t stream);
 int linear_dz_lines(int M, int N);
+// The whole backward pass of a small product in one kernel, in fp32 (dz is not
+// rounded); dx, dw and dbias may each be null.
+constexpr int kLinearSmall = 64;  // rows of x and columns of y, at most
+struct LinearSmallLaunch {
+  LinearDzLaunch e;  // dy, z and dbias
+  int K = 0;
+  const void* x = nullptr;
+  const void* w = nullptr;
+  long long ldx = 0, ldw = 0;
+  void* dx = nullptr;
+  void* dw = nullptr;
+  int32_t* status = nullptr;
+};
+cudaError_t launch_linear_small_backward(const LinearSmallLaunch& L, cudaStream_t stream);
 // out[i][c] = sum over lines l (in order) of table[i][l][c], i < tables.
 cudaError_t launch_sum_lines(const float* table, int tables, int lines, int H, float* out0,
                              float* out1, cudaStream_t stream);

@@ -678,6 +678,61 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzLaunch p) 
   }
 }
 
+// The backward pass of at most 64 rows and 64 columns of y, whole: blocks of 256 k x 8
+// rows of dx, then of 8 rows of dw. A block makes its part of dz in shared memory,
+// fp32 and not rounded, and a thread multiplies 2 columns of k. Bound by the launch
+// and by the contraction's few loads; the tiles would need four kernels.
+constexpr int kSmallRows = 8;
+__global__ void __launch_bounds__(128) linear_small_backward_kernel(const LinearSmallLaunch p) {
+  __shared__ float dz[kLinearSmall][kSmallRows];  // [contraction][row of the result]
+  const int M = p.e.M, N = p.e.N, tiles_x = p.dx != nullptr ? (M + kSmallRows - 1) / kSmallRows : 0;
+  const bool first = static_cast<int>(blockIdx.y) < tiles_x;  // rows of dx, else of dw
+  const int row0 = (first ? blockIdx.y : blockIdx.y - tiles_x) * kSmallRows;
+  const int len = first ? N : M, height = first ? M : N;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0;
+  for (int i = threadIdx.x; i < len * kSmallRows; i += 128) {
+    // neighbours along y's rows
+    const int r = first ? i / len : i % kSmallRows, c = first ? i - r * len : i / kSmallRows;
+    const int m = first ? row0 + r : c, n = first ? c : row0 + r;
+    float d = 0.0f;
+    if (row0 + r < height) {
+      const long long at = m * p.e.lddy + n;
+      d = p.e.dy_f32 ? static_cast<const float*>(p.e.dy)[at]
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(p.e.dy)[at]);
+      if (p.e.z != nullptr)
+        d *= linear_slope(__bfloat162float(static_cast<const __nv_bfloat16*>(p.e.z)[m * p.e.ldz + n]), p.e.act);
+    }
+    dz[c][r] = d;
+  }
+  __syncthreads();
+  if (!first && p.e.dbias != nullptr && blockIdx.x == 0 && threadIdx.x < kSmallRows &&
+      row0 + static_cast<int>(threadIdx.x) < N) {
+    float s = 0.0f;
+    for (int m = 0; m < M; ++m) s += dz[m][threadIdx.x];
+    p.e.dbias[row0 + threadIdx.x] = s;
+  }
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(first ? p.dx : p.dw);
+  const int k = blockIdx.x * 256 + threadIdx.x * 2;
+  if (out == nullptr || k >= p.K) return;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(first ? p.w : p.x) + k;
+  const long long ld = first ? p.ldw : p.ldx;
+  float a[kSmallRows][2] = {};
+#pragma unroll 8
+  for (int c = 0; c < len; ++c) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(src + c * ld);
+    const float lo = bf16lo_to_f32(v), hi = bf16hi_to_f32(v);
+#pragma unroll
+    for (int r = 0; r < kSmallRows; ++r) {
+      a[r][0] = fmaf(dz[c][r], lo, a[r][0]);
+      a[r][1] = fmaf(dz[c][r], hi, a[r][1]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kSmallRows; ++r)
+    if (row0 + r < height)
+      *reinterpret_cast<uint32_t*>(out + static_cast<long long>(row0 + r) * p.K + k) = pack_bf16x2(a[r][0], a[r][1]);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 lin_encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -931,6 +986,14 @@ cudaError_t launch_linear_dz(const LinearDzLaunch& L, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || L.lines == nullptr) return e;
   return launch_sum_lines(L.lines, 1, lines, L.N, L.dbias, nullptr, stream);
+}
+
+cudaError_t launch_linear_small_backward(const LinearSmallLaunch& L, cudaStream_t stream) {
+  const int tiles_x = L.dx != nullptr ? (L.e.M + kSmallRows - 1) / kSmallRows : 0;
+  const int tiles_w = L.dw != nullptr || L.e.dbias != nullptr ? (L.e.N + kSmallRows - 1) / kSmallRows : 0;
+  const dim3 grid((static_cast<unsigned>(L.K) + 255) / 256, static_cast<unsigned>(tiles_x + tiles_w));
+  linear_small_backward_kernel<<<grid, 128, 0, stream>>>(L);
+  return cudaGetLastError();
 }
 
 }  // namespace moe
