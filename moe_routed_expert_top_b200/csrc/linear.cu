@@ -632,6 +632,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzLaunch p) 
     __nv_bfloat16 v[V];
   };
   __shared__ float sum[8][32 * V + 1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int n = (blockIdx.x * 32 + lane) * V;
   const long long m0 = static_cast<long long>(p.M) * blockIdx.y / gridDim.y;
@@ -797,22 +798,22 @@ struct LinPlan {
 // With a tile for every pair: whole tiles of 256 x 256. (An output that leaves part
 // of the last turn idle is no slower for it: the operands' way from L2 is shared
 // by all, and cutting the last turn's tiles along k measured the same.) With
-// fewer: the tiles are cut along k into parts of g blocks, or are 128 or 64 wide,
-// or both, whichever has the least modelled time in SM clocks: a 128-wide k block
+// fewer: the tiles are cut along k into parts of g blocks, or are 128 or 64 wide
+// (each product for itself), or both, whichever has the least modelled time in SM clocks: a 128-wide k block
 // takes about 800 + 2.4 bn, an item 3000 beside its blocks, and parts a second
 // kernel, their sums written, read and added. An fp32 result is made of parts of
 // at most 16 blocks (2048 k) throughout.
 void lin_plan(const LinearProduct* L, int count, LinPlan* out) {
   const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
   double best = -1.0;
-  for (int width = kMaxBn; width >= 64; width /= 2) {
+  for (int width = 0; width < (count == 2 ? 9 : 3); ++width) {
     LinPlan p[2] = {};
     int kb[2] = {0, 0}, kb_most = 0;
     long long tiles = 0;
     bool fp32 = false;
     for (int i = 0; i < count; ++i) {
-      const int n32 = (L[i].N + 31) / 32 * 32;
-      p[i].bn = n32 < width ? n32 : width;
+      const int n32 = (L[i].N + 31) / 32 * 32, most = kMaxBn >> (i == 0 ? width % 3 : width / 3);
+      p[i].bn = n32 < most ? n32 : most;
       p[i].tiles_m = (L[i].M + 255) / 256;
       p[i].tiles_n = (L[i].N + p[i].bn - 1) / p[i].bn;
       kb[i] = (L[i].K + kBk - 1) / kBk;
@@ -822,7 +823,7 @@ void lin_plan(const LinearProduct* L, int count, LinPlan* out) {
     }
     const int least = fp32 ? (kb_most + 15) / 16 : 1;
     const int most = tiles < pairs ? least + 31 : least;
-    for (int cut = least; cut <= most; ++cut) {
+    for (int cut = least; cut <= most; cut += 1 + cut / 8) {
       const int g = (kb_most + cut - 1) / cut;
       if (cut > least && g < 2) break;
       long long items = 0;
@@ -847,7 +848,7 @@ void lin_plan(const LinearProduct* L, int count, LinPlan* out) {
         out[1] = q[1];
       }
     }
-    if (tiles >= pairs) break;
+    if (width == 0 && tiles >= pairs) break;
   }
 }
 

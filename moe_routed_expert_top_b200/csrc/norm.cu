@@ -60,28 +60,30 @@ __device__ __forceinline__ float weight_at(const void* w, int w_f32, int c, floa
                : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]);
 }
 
-// Sum of v over the threadIdx.x of this threadIdx.y; `slot` [2][blockDim.y][32]
-// floats, `flip` alternates so that one barrier a reduction is enough. All
-// threads of the block call it together.
+// Sums of v.x and v.y over the threadIdx.x of this threadIdx.y; `slot`
+// [2][blockDim.y][32] pairs, `flip` alternates so that one barrier a reduction is
+// enough. All threads of the block call it together. After the first step the
+// lower half of a warp carries one sum and the upper half the other: 6 shuffles
+// for the two and not 10.
 __device__ __forceinline__ float2 row_sum2(float2 v, float2* slot, int flip) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  const int nw = blockDim.x >> 5;
-  if (nw == 1) return v;
-  float2* s = slot + (flip * blockDim.y + threadIdx.y) * 32;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
   const int lane = threadIdx.x & 31;
-  v = lane < nw ? s[lane] : make_float2(0.0f, 0.0f);
+  const bool low = lane < 16;
+  float mine = (low ? v.x : v.y) + __shfl_xor_sync(0xffffffffu, low ? v.y : v.x, 16);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  const int nw = blockDim.x >> 5;
+  if (nw > 1) {
+    // [value][warp]
+    float* s = reinterpret_cast<float*>(slot + (flip * blockDim.y + threadIdx.y) * 32);
+    if ((lane & 15) == 0) s[(low ? 0 : 32) + (threadIdx.x >> 5)] = mine;
+    __syncthreads();
+    const int w = lane & 15;
+    mine = w < nw ? s[(low ? 0 : 32) + w] : 0.0f;
+    if (w + 16 < nw) mine += s[(low ? 0 : 32) + w + 16];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   }
-  return v;
+  return make_float2(__shfl_sync(0xffffffffu, mine, 0), __shfl_sync(0xffffffffu, mine, 16));
 }
 
 // The same for one value; `slot` [2][blockDim.y][32] floats.
@@ -405,6 +407,7 @@ __global__ void __launch_bounds__(kLong ? 1024 : 512, !kLong && kNormSlim<T, WT,
   }
   // the thread's weights: kept, or read (from L1) for each row before its second sum
   constexpr bool kKeep = !kLong;
+  const bool full = static_cast<int>(blockDim.x) * kEpt == p.H;  // every thread has 16 values
   Held<WT, V> gamma, beta;
 #pragma unroll
   for (int i = 0; i < kEpt / V; ++i)
@@ -451,7 +454,8 @@ __global__ void __launch_bounds__(kLong ? 1024 : 512, !kLong && kNormSlim<T, WT,
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       x[k] = add2(x[k], shift);
-      if constexpr (V == 1) {
+      if (full) {
+      } else if constexpr (V == 1) {
         const int c0 = 2 * k * blockDim.x + threadIdx.x;
         const float2 f = split(x[k]);
         x[k] = pair(c0 < p.H ? f.x : 0.0f, c0 + static_cast<int>(blockDim.x) < p.H ? f.y : 0.0f);
@@ -666,6 +670,7 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const
   __shared__ float2 slot[2 * 32];
   __shared__ uint64_t bars[kNormStages];
   const float inv = 1.0f / static_cast<float>(p.H);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const NormRows xs = norm_rows<T>(p.x, p.ldx, p.M, p.H), gs = norm_rows<T>(p.dy, p.ldy, p.M, p.H);
   const int half = stage_bytes / 2;
   auto ask = [&](int s, long long row) {
@@ -953,6 +958,9 @@ __global__ void __launch_bounds__(1024) sum_lines_kernel(const float* partial, i
                                                         float* out0, float* out1) {
   __shared__ float sum[32][33];
   float* out = blockIdx.y == 0 ? out0 : out1;
+  // launched while the kernel that writes the table ends
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (out == nullptr) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const long long c = static_cast<long long>(blockIdx.x) * 32 + lane;
@@ -973,9 +981,16 @@ __global__ void __launch_bounds__(1024) sum_lines_kernel(const float* partial, i
 
 cudaError_t launch_sum_lines(const float* table, int tables, int lines, int H, float* out0,
                              float* out1, cudaStream_t stream) {
-  const dim3 grid((static_cast<unsigned>(H) + 31) / 32, static_cast<unsigned>(tables));
-  sum_lines_kernel<<<grid, 1024, 0, stream>>>(table, lines, H, out0, out1);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((static_cast<unsigned>(H) + 31) / 32, static_cast<unsigned>(tables));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sum_lines_kernel, table, lines, H, out0, out1);
 }
 
 int norm_partial_rows(int M, int H) {
