@@ -13,14 +13,20 @@
 // from a difference of squares, so a large mean costs no digits. All sums are
 // fp32.
 //
-// A block is blockDim.y rows of blockDim.x threads (a multiple of 32); a thread
-// holds 16 values of its row, as vectors of V values where the row's length,
-// pitch and addresses allow 16-byte accesses, narrower ones where they do not.
-// Blocks stay and take every gridDim-th group of rows, and the next rows' values
-// are on their way while a row goes through its reductions.
-// Rows longer than 16 * 1024 (backward: 16 * 512) values do not fit the block's
-// registers and go to the *_wide kernels, which read a row again for each step
-// (from L2: a row is far smaller).
+// A thread holds 16 values of its row, as vectors of V values where the row's
+// length, pitch and addresses allow 16-byte accesses, narrower ones where they do
+// not, and works on them in pairs. Blocks stay and take every gridDim-th group of
+// rows. By a row's length:
+//   below 2 KB   norm_kernel, norm_bwd_kernel: up to 8 rows a block, the next ones'
+//                values on their way in registers (8192 x 500 bf16: 9.5 us forward,
+//                21 us backward; these are bound by the instructions)
+//   longer       norm_ring_kernel, norm_bwd_ring_kernel: one row a block, the next
+//                ones in shared memory (16383 x 2050 fp32 forward 55 us, 75% of the
+//                measured copy rate; 8192 x 7168 bf16 backward 78 us, 69%)
+//   above 16 * 1024 (backward: 16 * 512) values: too long for a block's registers;
+//                the *_wide kernels read a row again for each step (from L2)
+// At V = 1 (odd lengths of bf16) every value is an access of its own: 8192 x 4095
+// bf16 takes 62 us forward, 8192 x 4094 48 us.
 //
 // The weight gradients are sums over the rows: each block keeps its rows' sums
 // in registers, leaves them as one line of a [2][blocks][H] table and a second
@@ -41,7 +47,7 @@ namespace {
 constexpr int kEpt = 16;            // values of a row held by one thread
 constexpr int kNormMaxThreads = 1024;
 constexpr int kNormBwdMaxThreads = 512;
-constexpr int kShortRow = 2048;     // values of a row that shares its block with others, at most
+constexpr int kShortRow = 1024;     // values of a row below 2 KB, at most
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
@@ -100,183 +106,6 @@ __device__ __forceinline__ float row_sum(float v, float* slot, int flip) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
-}
-
-// V weights (gamma or beta) at column c as fp32.
-template <typename WT, int V>
-__device__ __forceinline__ void load_weights(const void* w, int c, float absent, float (&o)[V]) {
-  if (w == nullptr) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = absent;
-    return;
-  }
-  const Vec<WT, V> v = *reinterpret_cast<const Vec<WT, V>*>(static_cast<const WT*>(w) + c);
-#pragma unroll
-  for (int j = 0; j < V; ++j) o[j] = to_f32(v.v[j]);
-}
-
-// The thread's values of a row (on: there is one).
-template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* row, int H, bool on, Vec<T, V> (&v)[kEpt / V]) {
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    if (on && c < H) v[i] = *reinterpret_cast<const Vec<T, V>*>(row + c);
-  }
-}
-
-// Mean and 1 / standard deviation of the row that the block's threadIdx.x hold in
-// xv (values past the row: anything).
-template <typename T, int V>
-__device__ __forceinline__ void row_stats(const Vec<T, V> (&xv)[kEpt / V], int H, float inv, float eps,
-                                          float* slot, float& mean, float& rstd) {
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i) {
-    float t = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) t += to_f32(xv[i].v[j]);
-    s += (i * blockDim.x + threadIdx.x) * V < H ? t : 0.0f;
-  }
-  mean = row_sum(s, slot, 0) * inv;
-  float d2 = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i) {
-    float t = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float d = to_f32(xv[i].v[j]) - mean;
-      t = fmaf(d, d, t);
-    }
-    d2 += (i * blockDim.x + threadIdx.x) * V < H ? t : 0.0f;
-  }
-  rstd = rsqrtf(row_sum(d2, slot, 1) * inv + eps);
-}
-
-template <typename T, typename WT, int V>
-__device__ __forceinline__ void store_row(const NormLaunch& p, long long row, const Vec<T, V> (&xv)[kEpt / V],
-                                          float mean, float rstd) {
-  T* y = static_cast<T*>(p.y) + row * p.ldy;
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    if (c < p.H) {
-      float g[V], b[V];
-      load_weights<WT, V>(p.gamma, c, 1.0f, g);
-      load_weights<WT, V>(p.beta, c, 0.0f, b);
-      Vec<T, V> o;
-#pragma unroll
-      for (int j = 0; j < V; ++j) from_f32(o.v[j], (to_f32(xv[i].v[j]) - mean) * rstd * g[j] + b[j]);
-      *reinterpret_cast<Vec<T, V>*>(y + c) = o;
-    }
-  }
-}
-
-template <typename T, typename WT, int V>
-__global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormLaunch p) {
-  constexpr int NV = kEpt / V;
-  using VT = Vec<T, V>;
-  __shared__ float slot[2 * 32 * 8];
-  const float inv = 1.0f / static_cast<float>(p.H);
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.y;
-  const T* x = static_cast<const T*>(p.x);
-  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-  VT next[NV];
-  load_row<T, V>(x + (row < p.M ? row : 0) * p.ldx, p.H, row < p.M, next);
-  // every row group of the block runs the same number of turns (barriers inside)
-  for (long long base = row - threadIdx.y; base < p.M; base += stride, row += stride) {
-    const bool on = row < p.M;
-    VT xv[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) xv[i] = next[i];
-    const long long ahead = row + stride;
-    load_row<T, V>(x + (ahead < p.M ? ahead : 0) * p.ldx, p.H, ahead < p.M, next);
-    float mean, rstd;
-    row_stats<T, V>(xv, p.H, inv, p.eps, slot, mean, rstd);
-    if (!on) continue;
-    if (threadIdx.x == 0) {
-      if (p.mean != nullptr) p.mean[row] = mean;
-      if (p.rstd != nullptr) p.rstd[row] = rstd;
-    }
-    store_row<T, WT, V>(p, row, xv, mean, rstd);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Rows of 2 KB and more: whole rows come through a ring in shared memory, a bulk
-// copy each, so that 100 KB an SM and more are on their way whatever the threads
-// do. The block's barrier of a row's first sum tells that all have taken their
-// values; its first thread then asks for the row that goes in that place.
-//
-// A bulk copy takes whole 16-byte pieces. A row that does not begin and end at
-// such pieces (an odd length) is copied with the pieces around it, which belong to
-// its neighbours or to the gap between rows; only the matrix's first and last
-// row can begin or end in a piece that is not all the matrix's, and their few
-// values there are read one by one.
-// ---------------------------------------------------------------------------
-constexpr int kNormStages = 8;
-
-struct NormRows {
-  const uint8_t* base;  // first byte of the matrix
-  const uint8_t* end;   // behind its last
-  long long ld;         // bytes from row to row
-  int bytes;            // of a row
-};
-
-__device__ __forceinline__ const uint8_t* down16(const uint8_t* p) {
-  return reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(15));
-}
-__device__ __forceinline__ const uint8_t* up16(const uint8_t* p) { return down16(p + 15); }
-
-template <typename T>
-__device__ __forceinline__ NormRows norm_rows(const void* x, long long ld, int M, int H) {
-  NormRows r;
-  r.base = static_cast<const uint8_t*>(x);
-  r.ld = ld * static_cast<long long>(sizeof(T));
-  r.bytes = H * static_cast<int>(sizeof(T));
-  r.end = r.base + (M - 1) * r.ld + r.bytes;
-  return r;
-}
-
-// The 16-byte pieces of a row that lie in the matrix: [lo, hi).
-__device__ __forceinline__ void norm_span(const NormRows& r, long long row, const uint8_t*& lo, const uint8_t*& hi) {
-  const uint8_t* at = r.base + row * r.ld;
-  lo = down16(at);
-  hi = up16(at + r.bytes);
-  if (lo < r.base) lo = up16(r.base);
-  if (hi > r.end) hi = down16(r.end);
-}
-
-// Asks for a row (one thread). The row's place in `dst` (16-byte aligned) begins at
-// its address's offset from a 16-byte piece.
-__device__ __forceinline__ uint32_t norm_ask_bytes(const NormRows& r, long long row) {
-  const uint8_t *lo, *hi;
-  norm_span(r, row, lo, hi);
-  return static_cast<uint32_t>(hi - lo);
-}
-__device__ __forceinline__ void norm_ask(const NormRows& r, long long row, uint8_t* dst, uint32_t bar) {
-  const uint8_t *lo, *hi;
-  norm_span(r, row, lo, hi);
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst) + static_cast<uint32_t>(lo - down16(r.base + row * r.ld))),
-               "l"(lo), "r"(static_cast<uint32_t>(hi - lo)), "r"(bar)
-               : "memory");
-}
-
-// The values of the first and last row that no copy brings (whole block; a barrier
-// has to follow).
-template <typename T>
-__device__ __forceinline__ void norm_edges(const NormRows& r, long long row, uint8_t* dst) {
-  const uint8_t *lo, *hi;
-  norm_span(r, row, lo, hi);
-  const uint8_t* at = r.base + row * r.ld;
-  const int n = r.bytes / static_cast<int>(sizeof(T));
-  const int head = lo > at ? static_cast<int>((lo - at) / sizeof(T)) : 0;
-  const int tail = hi < at + r.bytes ? static_cast<int>((at + r.bytes - hi) / sizeof(T)) : 0;
-  T* out = reinterpret_cast<T*>(dst + (at - down16(at)));
-  const int t = threadIdx.x;
-  if (t < head) out[t] = reinterpret_cast<const T*>(at)[t];
-  if (t < tail) out[n - 1 - t] = reinterpret_cast<const T*>(at)[n - 1 - t];
 }
 
 // ---- two fp32 in one register pair (the row kernels are near the issue rate)
@@ -381,6 +210,270 @@ __device__ __forceinline__ void put_pairs(T* row, int H, const Pair (&f)[kEpt / 
   }
 }
 
+// Holds `absent` in place of weights that are not given.
+template <typename WT, int V>
+__device__ __forceinline__ void take_weights(const void* w, int H, float absent, Held<WT, V>& h) {
+  if (w != nullptr) {
+    take<WT, V>(static_cast<const WT*>(w), H, 0.0f, h);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEpt / V; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) from_f32(h.v[i].v[j], absent);
+  }
+}
+
+// Around the mean: x - mean where there is a value, 0 past the row; returns the sum
+// of the squares. `full`: every thread has 16 values.
+template <int V>
+__device__ __forceinline__ float center(Pair (&x)[kEpt / 2], float mean, int H, bool full) {
+  Pair q = both(0.0f);
+  const Pair shift = both(-mean);
+#pragma unroll
+  for (int k = 0; k < kEpt / 2; ++k) {
+    x[k] = add2(x[k], shift);
+    if (!full) {
+      if constexpr (V == 1) {
+        const int c0 = 2 * k * blockDim.x + threadIdx.x;
+        const float2 f = split(x[k]);
+        x[k] = pair(c0 < H ? f.x : 0.0f, c0 + static_cast<int>(blockDim.x) < H ? f.y : 0.0f);
+      } else {
+        if (static_cast<int>((k / (V / 2) * blockDim.x + threadIdx.x) * V) >= H) x[k] = both(0.0f);
+      }
+    }
+    q = fma2(x[k], x[k], q);
+  }
+  return sum(q);
+}
+
+__device__ __forceinline__ float sum_of(const Pair (&x)[kEpt / 2]) {
+  Pair s = x[0];
+#pragma unroll
+  for (int k = 1; k < kEpt / 2; ++k) s = add2(s, x[k]);
+  return sum(s);
+}
+
+// y = x rstd gamma + beta, in place.
+template <typename WT, int V>
+__device__ __forceinline__ void apply(Pair (&x)[kEpt / 2], float rstd, const Held<WT, V>& gamma,
+                                      const Held<WT, V>& beta) {
+  const Pair scale = both(rstd);
+#pragma unroll
+  for (int k = 0; k < kEpt / 2; ++k) x[k] = fma2(mul2(x[k], scale), pair_at(gamma, k), pair_at(beta, k));
+}
+
+// A row of the backward pass: xh and d = dy gamma from the row's values (dy 0 past
+// its end), the thread's part of sum(d) and sum(d xh); adds to the weight gradients.
+template <typename T, typename WT, int V>
+__device__ __forceinline__ float2 bwd_sums(const Held<T, V>& xv, const Held<T, V>& gv, const Held<WT, V>& gw,
+                                           float mean, float rstd, Pair (&xh)[kEpt / 2], Pair (&d)[kEpt / 2],
+                                           Pair (&dg)[kEpt / 2], Pair (&db)[kEpt / 2]) {
+  Pair s1 = both(0.0f), s2 = both(0.0f);
+  const Pair shift = both(-mean), scale = both(rstd);
+#pragma unroll
+  for (int k = 0; k < kEpt / 2; ++k) {
+    xh[k] = mul2(add2(pair_at(xv, k), shift), scale);
+    const Pair dy = pair_at(gv, k);
+    dg[k] = fma2(dy, xh[k], dg[k]);
+    db[k] = add2(db[k], dy);
+    d[k] = mul2(dy, pair_at(gw, k));
+    s1 = add2(s1, d[k]);
+    s2 = fma2(d[k], xh[k], s2);
+  }
+  return make_float2(sum(s1), sum(s2));
+}
+
+// dx = rstd (d - mean(d) - xh mean(d xh)), into d.
+__device__ __forceinline__ void bwd_dx(Pair (&d)[kEpt / 2], const Pair (&xh)[kEpt / 2], float2 s, float inv,
+                                       float rstd) {
+  const Pair c1 = both(-s.x * inv), c2 = both(-s.y * inv), scale = both(rstd);
+#pragma unroll
+  for (int k = 0; k < kEpt / 2; ++k) d[k] = mul2(fma2(xh[k], c2, add2(d[k], c1)), scale);
+}
+
+// ---------------------------------------------------------------------------
+// Rows below 2 KB: several to a block, the next ones' values on their way in
+// registers.
+// ---------------------------------------------------------------------------
+template <typename T, typename WT, int V>
+__global__ void __launch_bounds__(256, 3) norm_kernel(const NormLaunch p) {
+  constexpr int NP = kEpt / 2;
+  __shared__ float slot[2 * 32 * 8];
+  const float inv = 1.0f / static_cast<float>(p.H);
+  const bool full = static_cast<int>(blockDim.x) * kEpt == p.H;
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.y;
+  const T* x = static_cast<const T*>(p.x);
+  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  Held<WT, V> gamma, beta;
+  take_weights<WT, V>(p.gamma, p.H, 1.0f, gamma);
+  take_weights<WT, V>(p.beta, p.H, 0.0f, beta);
+  Held<T, V> next;
+  take<T, V>(x + (row < p.M ? row : 0) * p.ldx, row < p.M ? p.H : 0, 0.0f, next);
+  // every row group of the block runs the same number of turns (barriers inside)
+  for (long long base = row - threadIdx.y; base < p.M; base += stride, row += stride) {
+    Pair v[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) v[k] = pair_at(next, k);
+    const long long ahead = row + stride;
+    take<T, V>(x + (ahead < p.M ? ahead : 0) * p.ldx, ahead < p.M ? p.H : 0, 0.0f, next);
+    const float mean = row_sum(sum_of(v), slot, 0) * inv;
+    const float rstd = rsqrtf(row_sum(center<V>(v, mean, p.H, full), slot, 1) * inv + p.eps);
+    if (row >= p.M) continue;
+    if (threadIdx.x == 0) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+    apply<WT, V>(v, rstd, gamma, beta);
+    put_pairs<T, V>(static_cast<T*>(p.y) + row * p.ldy, p.H, v);
+  }
+}
+
+template <typename T, typename WT, int V>
+__global__ void __launch_bounds__(256, 2) norm_bwd_kernel(const NormLaunch p) {
+  constexpr int NP = kEpt / 2;
+  __shared__ float2 slot[2 * 32 * 8];
+  __shared__ float sums[2][kShortRow];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const float inv = 1.0f / static_cast<float>(p.H);
+  const T *x = static_cast<const T*>(p.x), *dy = static_cast<const T*>(p.dy);
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.y;
+  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  Held<WT, V> gw;
+  take_weights<WT, V>(p.gamma, p.H, 1.0f, gw);
+  Pair dg[NP], db[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) dg[k] = db[k] = both(0.0f);
+  Held<T, V> xn, gn;
+  float mean_next, rstd_next;
+  auto load = [&](long long r) {
+    const long long at = r < p.M ? r : 0;
+    const int H = r < p.M ? p.H : 0;
+    mean_next = __ldg(p.mean + at);
+    rstd_next = H > 0 ? __ldg(p.rstd + at) : 0.0f;
+    if (H == 0) mean_next = 0.0f;
+    take<T, V>(x + at * p.ldx, H, mean_next, xn);
+    take<T, V>(dy + at * p.ldy, H, 0.0f, gn);
+  };
+  load(row);
+  int flip = 0;
+  for (long long base = row - threadIdx.y; base < p.M; base += stride, row += stride) {
+    Pair xh[NP], d[NP];
+    const float mean = mean_next, rstd = rstd_next;
+    // (past the last row dy, the mean and rstd are 0, which adds nothing)
+    const float2 part = bwd_sums<T, WT, V>(xn, gn, gw, mean, rstd, xh, d, dg, db);
+    load(row + stride);
+    const float2 s = row_sum2(part, slot, flip);
+    flip ^= 1;
+    if (p.dx == nullptr || row >= p.M) continue;
+    bwd_dx(d, xh, s, inv, rstd);
+    put_pairs<T, V>(static_cast<T*>(p.dx) + row * p.lddx, p.H, d);
+  }
+  if (p.partial == nullptr) return;
+  // the block's row groups, in order
+  for (int y = 0; y < static_cast<int>(blockDim.y); ++y) {
+    if (static_cast<int>(threadIdx.y) == y) {
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int c0 = V == 1 ? 2 * k * blockDim.x + threadIdx.x
+                              : (k / (V > 1 ? V / 2 : 1) * blockDim.x + threadIdx.x) * V + 2 * (k % (V > 1 ? V / 2 : 1));
+        const int c1 = V == 1 ? c0 + blockDim.x : c0 + 1;
+        const float2 a = split(dg[k]), b = split(db[k]);
+        if (c0 < p.H) {
+          sums[0][c0] = y == 0 ? a.x : sums[0][c0] + a.x;
+          sums[1][c0] = y == 0 ? b.x : sums[1][c0] + b.x;
+        }
+        if (c1 < p.H) {
+          sums[0][c1] = y == 0 ? a.y : sums[0][c1] + a.y;
+          sums[1][c1] = y == 0 ? b.y : sums[1][c1] + b.y;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const int threads = blockDim.x * blockDim.y, t = threadIdx.y * blockDim.x + threadIdx.x;
+  for (int c = t; c < p.H; c += threads) {
+    p.partial[static_cast<long long>(blockIdx.x) * p.H + c] = sums[0][c];
+    p.partial[(static_cast<long long>(gridDim.x) + blockIdx.x) * p.H + c] = sums[1][c];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows of 2 KB and more: whole rows come through a ring in shared memory, a bulk
+// copy each, so that 100 KB an SM and more are on their way whatever the threads
+// do. The block's barrier of a row's first sum tells that all have taken their
+// values; its first thread then asks for the row that goes in that place.
+//
+// A bulk copy takes whole 16-byte pieces. A row that does not begin and end at
+// such pieces (an odd length) is copied with the pieces around it, which belong to
+// its neighbours or to the gap between rows; only the matrix's first and last
+// row can begin or end in a piece that is not all the matrix's, and their few
+// values there are read one by one.
+// ---------------------------------------------------------------------------
+constexpr int kNormStages = 8;
+
+struct NormRows {
+  const uint8_t* base;  // first byte of the matrix
+  const uint8_t* end;   // behind its last
+  long long ld;         // bytes from row to row
+  int bytes;            // of a row
+};
+
+__device__ __forceinline__ const uint8_t* down16(const uint8_t* p) {
+  return reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(15));
+}
+__device__ __forceinline__ const uint8_t* up16(const uint8_t* p) { return down16(p + 15); }
+
+template <typename T>
+__device__ __forceinline__ NormRows norm_rows(const void* x, long long ld, int M, int H) {
+  NormRows r;
+  r.base = static_cast<const uint8_t*>(x);
+  r.ld = ld * static_cast<long long>(sizeof(T));
+  r.bytes = H * static_cast<int>(sizeof(T));
+  r.end = r.base + (M - 1) * r.ld + r.bytes;
+  return r;
+}
+
+// The 16-byte pieces of a row that lie in the matrix: [lo, hi).
+__device__ __forceinline__ void norm_span(const NormRows& r, long long row, const uint8_t*& lo, const uint8_t*& hi) {
+  const uint8_t* at = r.base + row * r.ld;
+  lo = down16(at);
+  hi = up16(at + r.bytes);
+  if (lo < r.base) lo = up16(r.base);
+  if (hi > r.end) hi = down16(r.end);
+}
+
+// Asks for a row (one thread). The row's place in `dst` (16-byte aligned) begins at
+// its address's offset from a 16-byte piece.
+__device__ __forceinline__ uint32_t norm_ask_bytes(const NormRows& r, long long row) {
+  const uint8_t *lo, *hi;
+  norm_span(r, row, lo, hi);
+  return static_cast<uint32_t>(hi - lo);
+}
+__device__ __forceinline__ void norm_ask(const NormRows& r, long long row, uint8_t* dst, uint32_t bar) {
+  const uint8_t *lo, *hi;
+  norm_span(r, row, lo, hi);
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst) + static_cast<uint32_t>(lo - down16(r.base + row * r.ld))),
+               "l"(lo), "r"(static_cast<uint32_t>(hi - lo)), "r"(bar)
+               : "memory");
+}
+
+// The values of the first and last row that no copy brings (whole block; a barrier
+// has to follow).
+template <typename T>
+__device__ __forceinline__ void norm_edges(const NormRows& r, long long row, uint8_t* dst) {
+  const uint8_t *lo, *hi;
+  norm_span(r, row, lo, hi);
+  const uint8_t* at = r.base + row * r.ld;
+  const int n = r.bytes / static_cast<int>(sizeof(T));
+  const int head = lo > at ? static_cast<int>((lo - at) / sizeof(T)) : 0;
+  const int tail = hi < at + r.bytes ? static_cast<int>((at + r.bytes - hi) / sizeof(T)) : 0;
+  T* out = reinterpret_cast<T*>(dst + (at - down16(at)));
+  const int t = threadIdx.x;
+  if (t < head) out[t] = reinterpret_cast<const T*>(at)[t];
+  if (t < tail) out[n - 1 - t] = reinterpret_cast<const T*>(at)[n - 1 - t];
+}
+
 // kLong: rows of more than 8192 values, whose 1024 threads have 64 registers each.
 // Else a thread keeps its weights over the rows: two blocks of 512 threads share an
 // SM where a kept weight is half a register, one where it is a whole one.
@@ -409,16 +502,9 @@ __global__ void __launch_bounds__(kLong ? 1024 : 512, !kLong && kNormSlim<T, WT,
   constexpr bool kKeep = !kLong;
   const bool full = static_cast<int>(blockDim.x) * kEpt == p.H;  // every thread has 16 values
   Held<WT, V> gamma, beta;
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      from_f32(gamma.v[i].v[j], 1.0f);
-      from_f32(beta.v[i].v[j], 0.0f);
-    }
   if (kKeep) {
-    if (p.gamma != nullptr) take<WT, V>(static_cast<const WT*>(p.gamma), p.H, 0.0f, gamma);
-    if (p.beta != nullptr) take<WT, V>(static_cast<const WT*>(p.beta), p.H, 0.0f, beta);
+    take_weights<WT, V>(p.gamma, p.H, 1.0f, gamma);
+    take_weights<WT, V>(p.beta, p.H, 0.0f, beta);
   }
   __syncthreads();
   int stage = 0;
@@ -439,43 +525,24 @@ __global__ void __launch_bounds__(kLong ? 1024 : 512, !kLong && kNormSlim<T, WT,
 #pragma unroll
       for (int k = 0; k < NP; ++k) x[k] = pair_at(held, k);
     }
-    Pair s = x[0];
-#pragma unroll
-    for (int k = 1; k < NP; ++k) s = add2(s, x[k]);
-    const float mean = row_sum(sum(s), slot, 0) * inv;
+    const float mean = row_sum(sum_of(x), slot, 0) * inv;
     __syncwarp();
     if (threadIdx.x == 0) ask(stage, row + static_cast<long long>(stages) * gridDim.x);
     if (++stage == stages) {
       stage = 0;
       phase ^= 1u;
     }
-    Pair q = both(0.0f);
-    const Pair shift = both(-mean);
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      x[k] = add2(x[k], shift);
-      if (full) {
-      } else if constexpr (V == 1) {
-        const int c0 = 2 * k * blockDim.x + threadIdx.x;
-        const float2 f = split(x[k]);
-        x[k] = pair(c0 < p.H ? f.x : 0.0f, c0 + static_cast<int>(blockDim.x) < p.H ? f.y : 0.0f);
-      } else {
-        if (static_cast<int>((k / (V / 2) * blockDim.x + threadIdx.x) * V) >= p.H) x[k] = both(0.0f);
-      }
-      q = fma2(x[k], x[k], q);
-    }
+    const float q = center<V>(x, mean, p.H, full);
     if (!kKeep) {
-      if (p.gamma != nullptr) take<WT, V>(static_cast<const WT*>(p.gamma), p.H, 0.0f, gamma);
-      if (p.beta != nullptr) take<WT, V>(static_cast<const WT*>(p.beta), p.H, 0.0f, beta);
+      take_weights<WT, V>(p.gamma, p.H, 1.0f, gamma);
+      take_weights<WT, V>(p.beta, p.H, 0.0f, beta);
     }
-    const float rstd = rsqrtf(row_sum(sum(q), slot, 1) * inv + p.eps);
+    const float rstd = rsqrtf(row_sum(q, slot, 1) * inv + p.eps);
     if (threadIdx.x == 0) {
       if (p.mean != nullptr) p.mean[row] = mean;
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
-    const Pair scale = both(rstd);
-#pragma unroll
-    for (int k = 0; k < NP; ++k) x[k] = fma2(mul2(x[k], scale), pair_at(gamma, k), pair_at(beta, k));
+    apply<WT, V>(x, rstd, gamma, beta);
     put_pairs<T, V>(static_cast<T*>(p.y) + row * p.ldy, p.H, x);
   }
 }
@@ -506,161 +573,6 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_wide_kernel(const NormLa
                        weight_at(p.beta, p.w_f32, c, 0.0f));
 }
 
-// A thread's weights (as stored: bf16 ones take half the registers) and zeros for
-// its sums of the weight gradients.
-template <typename WT, int V>
-__device__ __forceinline__ void bwd_start(const NormLaunch& p, Vec<WT, V> (&gw)[kEpt / V], float (&dg)[kEpt / V][V],
-                                          float (&db)[kEpt / V][V]) {
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      dg[i][j] = db[i][j] = 0.0f;
-      from_f32(gw[i].v[j], 1.0f);
-    }
-    if (p.gamma != nullptr && c < p.H)
-      gw[i] = *reinterpret_cast<const Vec<WT, V>*>(static_cast<const WT*>(p.gamma) + c);
-  }
-}
-
-// The thread's part of sum(g), sum(g xh); adds to its weight gradients.
-template <typename T, typename WT, int V>
-__device__ __forceinline__ float2 bwd_sums(const Vec<T, V> (&xv)[kEpt / V], const Vec<T, V> (&gv)[kEpt / V],
-                                           const Vec<WT, V> (&gw)[kEpt / V], float mean, float rstd, int H,
-                                           float (&dg)[kEpt / V][V], float (&db)[kEpt / V][V]) {
-  float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i) {
-    if ((i * blockDim.x + threadIdx.x) * V < H)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float d = to_f32(gv[i].v[j]);
-        const float xh = (to_f32(xv[i].v[j]) - mean) * rstd;
-        const float g = __fmul_rn(d, to_f32(gw[i].v[j]));  // the same value below: its mean cancels in a row of one
-        s.x += g;
-        s.y = fmaf(g, xh, s.y);
-        dg[i][j] = fmaf(d, xh, dg[i][j]);
-        db[i][j] += d;
-      }
-  }
-  return s;
-}
-
-template <typename T, typename WT, int V>
-__device__ __forceinline__ void bwd_store(const NormLaunch& p, long long row, const Vec<T, V> (&xv)[kEpt / V],
-                                          const Vec<T, V> (&gv)[kEpt / V], const Vec<WT, V> (&gw)[kEpt / V],
-                                          float mean, float rstd, float c1, float c2) {
-  T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    if (c < p.H) {
-      Vec<T, V> o;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float xh = (to_f32(xv[i].v[j]) - mean) * rstd;
-        from_f32(o.v[j], rstd * (__fmul_rn(to_f32(gv[i].v[j]), to_f32(gw[i].v[j])) - c1 - xh * c2));
-      }
-      *reinterpret_cast<Vec<T, V>*>(dx + c) = o;
-    }
-  }
-}
-
-// One line of the [2][lines][H] table.
-template <int V>
-__device__ __forceinline__ void bwd_lines(const NormLaunch& p, long long line, long long lines,
-                                          const float (&dg)[kEpt / V][V], const float (&db)[kEpt / V][V]) {
-  float* pg = p.partial + line * p.H;
-  float* pb = p.partial + (lines + line) * p.H;
-  constexpr int W = V < 4 ? V : 4;  // (a line starts at a multiple of V floats)
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    if (c < p.H)
-#pragma unroll
-      for (int j = 0; j < V; j += W) {
-        Vec<float, W> a, b;
-#pragma unroll
-        for (int q = 0; q < W; ++q) {
-          a.v[q] = dg[i][j + q];
-          b.v[q] = db[i][j + q];
-        }
-        *reinterpret_cast<Vec<float, W>*>(pg + c + j) = a;
-        *reinterpret_cast<Vec<float, W>*>(pb + c + j) = b;
-      }
-  }
-}
-
-// A row's values of the backward pass, as they are loaded.
-template <typename T, int V>
-struct BwdRow {
-  Vec<T, V> x[kEpt / V], g[kEpt / V];
-  float mean, rstd;
-};
-template <typename T, int V>
-__device__ __forceinline__ void load_bwd_row(const NormLaunch& p, long long row, BwdRow<T, V>& r) {
-  const bool on = row < p.M;
-  const long long at = on ? row : 0;
-  load_row<T, V>(static_cast<const T*>(p.x) + at * p.ldx, p.H, on, r.x);
-  load_row<T, V>(static_cast<const T*>(p.dy) + at * p.ldy, p.H, on, r.g);
-  r.mean = on ? __ldg(p.mean + at) : 0.0f;
-  r.rstd = on ? __ldg(p.rstd + at) : 0.0f;
-}
-
-template <typename T, typename WT, int V>
-__global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_kernel(const NormLaunch p) {
-  constexpr int NV = kEpt / V;
-  __shared__ float2 slot[2 * 32 * 8];
-  const float inv = 1.0f / static_cast<float>(p.H);
-  float dg[NV][V], db[NV][V];
-  Vec<WT, V> gw[NV];
-  bwd_start<WT, V>(p, gw, dg, db);
-  int flip = 0;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.y;
-  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-  BwdRow<T, V> next;
-  load_bwd_row<T, V>(p, row, next);
-  // every row group of the block runs the same number of turns (barriers inside)
-  for (long long base = row - threadIdx.y; base < p.M; base += stride, row += stride) {
-    const bool on = row < p.M;
-    const BwdRow<T, V> cur = next;
-    load_bwd_row<T, V>(p, row + stride, next);
-    float2 s = bwd_sums<T, WT, V>(cur.x, cur.g, gw, cur.mean, cur.rstd, on ? p.H : 0, dg, db);
-    if (p.dx == nullptr) continue;
-    s = row_sum2(s, slot, flip);
-    flip ^= 1;
-    if (on) bwd_store<T, WT, V>(p, row, cur.x, cur.g, gw, cur.mean, cur.rstd, s.x * inv, s.y * inv);
-  }
-  if (p.partial == nullptr) return;
-  if (blockDim.y == 1) {
-    bwd_lines<V>(p, blockIdx.x, gridDim.x, dg, db);
-    return;
-  }
-  // the block's row groups first, in order (H <= 2048 where there are several)
-  __shared__ float sums[2][kShortRow];
-  for (int y = 0; y < static_cast<int>(blockDim.y); ++y) {
-    if (static_cast<int>(threadIdx.y) == y) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c < p.H)
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            sums[0][c + j] = y == 0 ? dg[i][j] : sums[0][c + j] + dg[i][j];
-            sums[1][c + j] = y == 0 ? db[i][j] : sums[1][c + j] + db[i][j];
-          }
-      }
-    }
-    __syncthreads();
-  }
-  const int threads = blockDim.x * blockDim.y, t = threadIdx.y * blockDim.x + threadIdx.x;
-  for (int c = t; c < p.H; c += threads) {
-    p.partial[static_cast<long long>(blockIdx.x) * p.H + c] = sums[0][c];
-    p.partial[(static_cast<long long>(gridDim.x) + blockIdx.x) * p.H + c] = sums[1][c];
-  }
-}
-
 // The same through a ring of whole rows (see norm_ring_kernel), x's and dy's.
 template <typename T, typename WT, int V>
 __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const NormLaunch p, int stages,
@@ -686,14 +598,10 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const
     for (int s = 0; s < stages; ++s) ask(s, blockIdx.x + static_cast<long long>(s) * gridDim.x);
   }
   Held<WT, V> gw;
+  take_weights<WT, V>(p.gamma, p.H, 1.0f, gw);
   Pair dg[NP], db[NP];
 #pragma unroll
   for (int k = 0; k < NP; ++k) dg[k] = db[k] = both(0.0f);
-#pragma unroll
-  for (int i = 0; i < kEpt / V; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) from_f32(gw.v[i].v[j], 1.0f);
-  if (p.gamma != nullptr) take<WT, V>(static_cast<const WT*>(p.gamma), p.H, 0.0f, gw);
   __syncthreads();
   int stage = 0, flip = 0;
   uint32_t phase = 0;
@@ -714,22 +622,10 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const
     const uint8_t *xa = xs.base + row * xs.ld, *ga = gs.base + row * gs.ld;
     Pair xh[NP], d[NP];
     Held<T, V> xv, gv;
-    // past the row dy = 0, which adds nothing to any sum
-    take<T, V>(reinterpret_cast<const T*>(place + (xa - down16(xa))), p.H, 0.0f, xv);
+    // past the row dy = 0 and xh about 0: nothing for any sum
+    take<T, V>(reinterpret_cast<const T*>(place + (xa - down16(xa))), p.H, mean, xv);
     take<T, V>(reinterpret_cast<const T*>(place + half + (ga - down16(ga))), p.H, 0.0f, gv);
-    Pair s1 = both(0.0f), s2 = both(0.0f);
-    const Pair shift = both(-mean), scale = both(rstd);
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      xh[k] = mul2(add2(pair_at(xv, k), shift), scale);
-      const Pair dy = pair_at(gv, k);
-      dg[k] = fma2(dy, xh[k], dg[k]);
-      db[k] = add2(db[k], dy);
-      d[k] = mul2(dy, pair_at(gw, k));
-      s1 = add2(s1, d[k]);
-      s2 = fma2(d[k], xh[k], s2);
-    }
-    const float2 s = row_sum2(make_float2(sum(s1), sum(s2)), slot, flip);
+    const float2 s = row_sum2(bwd_sums<T, WT, V>(xv, gv, gw, mean, rstd, xh, d, dg, db), slot, flip);
     flip ^= 1;
     __syncwarp();
     if (threadIdx.x == 0) ask(stage, row + static_cast<long long>(stages) * gridDim.x);
@@ -738,9 +634,7 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const
       phase ^= 1u;
     }
     if (p.dx != nullptr) {
-      const Pair c1 = both(-s.x * inv), c2 = both(-s.y * inv);
-#pragma unroll
-      for (int k = 0; k < NP; ++k) d[k] = mul2(fma2(xh[k], c2, add2(d[k], c1)), scale);
+      bwd_dx(d, xh, s, inv, rstd);
       put_pairs<T, V>(static_cast<T*>(p.dx) + row * p.lddx, p.H, d);
     }
   }
@@ -827,8 +721,8 @@ dim3 norm_block(int H) {
 
 bool norm_bwd_wide(int H) { return H > kEpt * kNormBwdMaxThreads; }
 
-// Blocks that stay: what an SM holds at 64 registers a thread (forward), at 128
-// (backward, where a block's sums are a line of the table each).
+// Blocks that stay: what an SM holds at 85 registers a thread (forward, short
+// rows), at 128 (backward, where a block's sums are a line of the table each).
 int norm_blocks(int M, const dim3& b, int registers) {
   const long long need = (static_cast<long long>(M) + b.y - 1) / b.y;
   const int threads = static_cast<int>(b.x * b.y);
@@ -883,7 +777,7 @@ cudaError_t norm_forward_launch(const NormLaunch& L, cudaStream_t stream) {
                ? norm_ring_launch<norm_ring_kernel<T, WT, V, true>>(L, grid, threads, stages, 1, stream)
                : norm_ring_launch<norm_ring_kernel<T, WT, V, false>>(L, grid, threads, stages, 1, stream);
   }
-  norm_kernel<T, WT, V><<<static_cast<unsigned>(norm_blocks(L.M, b, 64)), b, 0, stream>>>(L);
+  norm_kernel<T, WT, V><<<static_cast<unsigned>(norm_blocks(L.M, b, 85)), b, 0, stream>>>(L);
   return cudaGetLastError();
 }
 
