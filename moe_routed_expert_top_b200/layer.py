@@ -181,10 +181,15 @@ def _on_device_of(t: torch.Tensor):
     return torch.cuda.device(t.device)
 
 
+# (the handle alone; torch.cuda.current_stream builds an object around it, which costs
+# a tenth of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream_of(t: torch.Tensor) -> int:
-    """The current stream of the tensor's device. (Asked for by index: without one,
-    torch takes longer to find the index than the rest of a small call.)"""
-    return torch.cuda.current_stream(t.get_device()).cuda_stream
+    """The current stream of the tensor's device."""
+    return _raw_stream(t.get_device())
 
 
 def _matrix(t: torch.Tensor, name: str, shape, dtypes, device) -> int:
@@ -439,7 +444,7 @@ class LayerNorm:
         ldy = 0 if out is None else _matrix(out, "out", x.shape, (x.dtype,), x.device)
         with _on_device_of(x):
             if out is None:
-                out = torch.empty(M, H, dtype=x.dtype, device=x.device)
+                out = torch.empty_like(x, memory_format=torch.contiguous_format)
             mean = rstd = None
             if stats:
                 mean = torch.empty(M, dtype=torch.float32, device=x.device)
