@@ -39,6 +39,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cstring>
 #include <mutex>
 #include <type_traits>
 
@@ -620,10 +621,12 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 
 // dz = dy * act'(z), rounded to bf16 (the MMA's operand type; dbias takes the
 // unrounded values), and the column sums of a block's rows. A thread has V
-// columns, a block's 8 warps every eighth row. Bound by HBM: one pass.
+// columns, a block's 8 warps every eighth row. One pass, bound by HBM and by the
+// slope's arithmetic: a kernel for each activation, so that no branch parts a row's
+// values, and the loads of a warp's next rows together.
 constexpr int kDzLines = 1024;  // blocks along M, at most
-template <int V, bool kF32>
-__global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzLaunch p) {
+template <int V, bool kF32, int kAct>
+__global__ void __launch_bounds__(256, 3) linear_dz_kernel(const LinearDzLaunch p) {
   using Dy = typename std::conditional<kF32, float, __nv_bfloat16>::type;
   struct alignas(sizeof(Dy) * V > 16 ? 16 : sizeof(Dy) * V) DyV {
     Dy v[V];
@@ -631,42 +634,60 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzLaunch p) 
   struct alignas(2 * V) ZV {
     __nv_bfloat16 v[V];
   };
+  constexpr int kRows = V == 1 ? 4 : 2;  // a warp's loads in flight together
   __shared__ float sum[8][32 * V + 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int n = (blockIdx.x * 32 + lane) * V;
   const long long m0 = static_cast<long long>(p.M) * blockIdx.y / gridDim.y;
   const long long m1 = static_cast<long long>(p.M) * (blockIdx.y + 1) / gridDim.y;
-  float s[V];
+  Pair s[(V + 1) / 2];  // (V = 1: the first of the pair)
 #pragma unroll
-  for (int i = 0; i < V; ++i) s[i] = 0.0f;
+  for (int i = 0; i < (V + 1) / 2; ++i) s[i] = both(0.0f);
   if (n < p.N) {
     const Dy* dy = static_cast<const Dy*>(p.dy) + n;
     const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(p.z) + n;
-#pragma unroll 4
-    for (long long m = m0 + w; m < m1; m += 8) {
-      const DyV d = *reinterpret_cast<const DyV*>(dy + m * p.lddy);
-      float f[V];
+    for (long long first = m0 + w; first < m1; first += 8 * kRows) {
+      DyV d[kRows];
+      ZV zv[kRows];
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = static_cast<float>(d.v[i]);
-      if (p.z != nullptr) {
-        const ZV zv = *reinterpret_cast<const ZV*>(z + m * p.ldz);
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] *= linear_slope(__bfloat162float(zv.v[i]), p.act);
+      for (int a = 0; a < kRows; ++a) {
+        const long long m = first + 8 * a;
+        if (m >= m1) break;
+        d[a] = *reinterpret_cast<const DyV*>(dy + m * p.lddy);
+        if (kAct != kActNone) zv[a] = *reinterpret_cast<const ZV*>(z + m * p.ldz);
       }
-      if (p.dz != nullptr) {
+#pragma unroll
+      for (int a = 0; a < kRows; ++a) {
+        const long long m = first + 8 * a;
+        if (m >= m1) break;
         ZV o;
+        if constexpr (V == 1) {
+          float f = static_cast<float>(d[a].v[0]);
+          if (kAct != kActNone) f *= linear_slope(__bfloat162float(zv[a].v[0]), kAct);
+          s[0] = add2(s[0], pair(f, 0.0f));
+          o.v[0] = __float2bfloat16(f);
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) o.v[i] = __float2bfloat16(f[i]);
-        *reinterpret_cast<ZV*>(static_cast<__nv_bfloat16*>(p.dz) + m * p.lddz + n) = o;
+          for (int i = 0; i < V / 2; ++i) {
+            Pair f = pair(static_cast<float>(d[a].v[2 * i]), static_cast<float>(d[a].v[2 * i + 1]));
+            if (kAct != kActNone)
+              f = mul2(f, linear_slope2<kAct>(make_float2(__bfloat162float(zv[a].v[2 * i]),
+                                                          __bfloat162float(zv[a].v[2 * i + 1]))));
+            s[i] = add2(s[i], f);
+            const float2 g = split(f);
+            const uint32_t w2 = pack_bf16x2(g.x, g.y);
+            memcpy(&o.v[2 * i], &w2, 4);
+          }
+        }
+        if (p.dz != nullptr)
+          *reinterpret_cast<ZV*>(static_cast<__nv_bfloat16*>(p.dz) + m * p.lddz + n) = o;
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] += f[i];
     }
   }
   if (p.lines == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < V; ++i) sum[w][i * 32 + lane] = s[i];
+  for (int i = 0; i < V; ++i) sum[w][i * 32 + lane] = i & 1 ? split(s[i / 2]).y : split(s[i / 2]).x;
   __syncthreads();
   for (int i = threadIdx.x; i < 32 * V; i += 256) {
     const int c = (blockIdx.x * 32 + (i & 31)) * V + (i >> 5);
@@ -960,13 +981,23 @@ cudaError_t launch_linear_gemm(const LinearProduct* L, int count, float* partial
   return e;
 }
 
-// Lines (blocks along M) that give about four blocks an SM, of at least 8 rows.
+// Lines (blocks along M) that give three blocks an SM, what it holds, of at least 8 rows.
 int linear_dz_lines(int M, int N) {
   const int cols = (N + 255) / 256 > 0 ? (N + 255) / 256 : 1;
-  int n = (4 * device_sm_count() + cols - 1) / cols;
+  int n = 3 * device_sm_count() / cols;
   if (n > (M + 7) / 8) n = (M + 7) / 8;
   if (n > kDzLines) n = kDzLines;
   return n > 0 ? n : 1;
+}
+
+template <int V, bool kF32>
+static void dz_launch(const LinearDzLaunch& L, const dim3& grid, cudaStream_t stream) {
+  switch (L.z != nullptr ? L.act : kActNone) {
+    case kActRelu: linear_dz_kernel<V, kF32, kActRelu><<<grid, 256, 0, stream>>>(L); break;
+    case kActSilu: linear_dz_kernel<V, kF32, kActSilu><<<grid, 256, 0, stream>>>(L); break;
+    case kActGelu: linear_dz_kernel<V, kF32, kActGelu><<<grid, 256, 0, stream>>>(L); break;
+    default: linear_dz_kernel<V, kF32, kActNone><<<grid, 256, 0, stream>>>(L); break;
+  }
 }
 
 cudaError_t launch_linear_dz(const LinearDzLaunch& L, cudaStream_t stream) {
@@ -979,11 +1010,9 @@ cudaError_t launch_linear_dz(const LinearDzLaunch& L, cudaStream_t stream) {
   const int cols = wide ? 256 : 32;
   const dim3 grid((static_cast<unsigned>(L.N) + cols - 1) / cols, static_cast<unsigned>(lines));
   if (wide)
-    L.dy_f32 ? linear_dz_kernel<8, true><<<grid, 256, 0, stream>>>(L)
-             : linear_dz_kernel<8, false><<<grid, 256, 0, stream>>>(L);
+    L.dy_f32 ? dz_launch<8, true>(L, grid, stream) : dz_launch<8, false>(L, grid, stream);
   else
-    L.dy_f32 ? linear_dz_kernel<1, true><<<grid, 256, 0, stream>>>(L)
-             : linear_dz_kernel<1, false><<<grid, 256, 0, stream>>>(L);
+    L.dy_f32 ? dz_launch<1, true>(L, grid, stream) : dz_launch<1, false>(L, grid, stream);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || L.lines == nullptr) return e;
   return launch_sum_lines(L.lines, 1, lines, L.N, L.dbias, nullptr, stream);

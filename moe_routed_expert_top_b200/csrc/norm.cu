@@ -38,6 +38,7 @@
 #include <cstring>
 
 #include "internal.h"
+#include "pair.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -108,38 +109,6 @@ __device__ __forceinline__ float row_sum(float v, float* slot, int flip) {
   return v;
 }
 
-// ---- two fp32 in one register pair (the row kernels are near the issue rate)
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
-__device__ __forceinline__ float2 split(Pair p) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ float sum(Pair p) {
-  const float2 f = split(p);
-  return f.x + f.y;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-  Pair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // A pair of stored values.
 __device__ __forceinline__ Pair pair_of(const __nv_bfloat16* v) {
   uint32_t w;
