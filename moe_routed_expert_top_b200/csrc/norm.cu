@@ -18,15 +18,15 @@
 // not, and works on them in pairs. Blocks stay and take every gridDim-th group of
 // rows. By a row's length:
 //   below 2 KB   norm_kernel, norm_bwd_kernel: up to 8 rows a block, the next ones'
-//                values on their way in registers (8192 x 500 bf16: 9.5 us forward,
+//                values on their way in registers (8192 x 500 bf16: 8.6 us forward,
 //                21 us backward; these are bound by the instructions)
-//   longer       norm_ring_kernel, norm_bwd_ring_kernel: one row a block, the next
-//                ones in shared memory (16383 x 2050 fp32 forward 55 us, 75% of the
-//                measured copy rate; 8192 x 7168 bf16 backward 78 us, 69%)
+//   longer       norm_ring_kernel, norm_bwd_ring_kernel: the next rows in shared
+//                memory; two rows a turn forward (16383 x 2050 fp32 46 us, 90% of
+//                the measured copy rate), one backward (8192 x 7168 bf16 78 us, 69%)
 //   above 16 * 1024 (backward: 16 * 512) values: too long for a block's registers;
 //                the *_wide kernels read a row again for each step (from L2)
 // At V = 1 (odd lengths of bf16) every value is an access of its own: 8192 x 4095
-// bf16 takes 62 us forward, 8192 x 4094 48 us.
+// bf16 takes 57 us forward, 8192 x 4094 38 us.
 //
 // The weight gradients are sums over the rows: each block keeps its rows' sums
 // in registers, leaves them as one line of a [2][blocks][H] table and a second
@@ -87,8 +87,10 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* slot, int flip) {
     const int w = lane & 15;
     mine = w < nw ? s[(low ? 0 : 32) + w] : 0.0f;
     if (w + 16 < nw) mine += s[(low ? 0 : 32) + w + 16];
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (nw > 8) mine += __shfl_xor_sync(0xffffffffu, mine, 8);
+    if (nw > 4) mine += __shfl_xor_sync(0xffffffffu, mine, 4);
+    mine += __shfl_xor_sync(0xffffffffu, mine, 2);
+    mine += __shfl_xor_sync(0xffffffffu, mine, 1);
   }
   return make_float2(__shfl_sync(0xffffffffu, mine, 0), __shfl_sync(0xffffffffu, mine, 16));
 }
@@ -102,11 +104,23 @@ __device__ __forceinline__ float row_sum(float v, float* slot, int flip) {
   float* s = slot + (flip * blockDim.y + threadIdx.y) * 32;
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  v = lane < nw ? s[lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  if (nw <= 4) {  // every four lanes add up all of them, and so on
+    const int w = threadIdx.x & 3;
+    v = w < nw ? s[w] : 0.0f;
+  } else if (nw <= 16) {
+    const int w = threadIdx.x & 15;
+    v = w < nw ? s[w] : 0.0f;
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+  } else {
+    const int w = threadIdx.x & 31;
+    v = w < nw ? s[w] : 0.0f;
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+  }
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  return v + __shfl_xor_sync(0xffffffffu, v, 1);
 }
 
 // A pair of stored values.
@@ -411,6 +425,12 @@ __device__ __forceinline__ void norm_span(const NormRows& r, long long row, cons
   if (hi > r.end) hi = down16(r.end);
 }
 
+// A row's arrival. (Most have arrived: the bounded wait reads the time first, which
+// costs more than the rest of it.)
+__device__ __forceinline__ void norm_wait(uint32_t bar, uint32_t phase) {
+  if (!mbar_try_wait(bar, phase)) mbar_wait_drain(bar, phase);
+}
+
 // Asks for a row (one thread). The row's place in `dst` (16-byte aligned) begins at
 // its address's offset from a 16-byte piece.
 __device__ __forceinline__ uint32_t norm_ask_bytes(const NormRows& r, long long row) {
@@ -443,76 +463,105 @@ __device__ __forceinline__ void norm_edges(const NormRows& r, long long row, uin
   if (t < tail) out[n - 1 - t] = reinterpret_cast<const T*>(at)[n - 1 - t];
 }
 
-// kLong: rows of more than 8192 values, whose 1024 threads have 64 registers each.
-// Else a thread keeps its weights over the rows: two blocks of 512 threads share an
-// SM where a kept weight is half a register, one where it is a whole one.
-template <typename T, typename WT, int V>
-constexpr bool kNormSlim = sizeof(T) == 2 && sizeof(WT) == 2 && V > 1;
-template <typename T, typename WT, int V, bool kLong>
-__global__ void __launch_bounds__(kLong ? 1024 : 512, !kLong && kNormSlim<T, WT, V> ? 2 : 1)
-    norm_ring_kernel(const NormLaunch p, int stages, int stage_bytes) {
+// A block takes kRows neighbouring rows a turn: with two, one barrier and half the
+// shuffles serve both rows' sums, and the weights are widened once for both (16384 x
+// 2048 bf16: 35 us with one, 28 us with two). Rows of more than 8192 values, whose
+// 1024 threads have 64 registers each, come one by one, and their weights are read
+// (from L1) for each; else a thread keeps its weights.
+template <typename T, typename WT, int V, int kRows>
+__global__ void __launch_bounds__(kRows == 1 ? 1024 : 512) norm_ring_kernel(const NormLaunch p, int stages,
+                                                                           int stage_bytes) {
   constexpr int NP = kEpt / 2;
   extern __shared__ __align__(128) uint8_t norm_smem[];
-  __shared__ float slot[2 * 32];
+  __shared__ float2 slot[2 * 32];
   __shared__ uint64_t bars[kNormStages];
   const float inv = 1.0f / static_cast<float>(p.H);
   const NormRows rows = norm_rows<T>(p.x, p.ldx, p.M, p.H);
-  auto ask = [&](int s, long long row) {
+  const int half = stage_bytes / kRows;
+  auto ask = [&](int s, long long turn) {
+    const long long row = turn * kRows;
     if (row >= p.M) return;
-    mbar_arrive_expect_tx(smem_u32(bars + s), norm_ask_bytes(rows, row));
-    norm_ask(rows, row, norm_smem + s * stage_bytes, smem_u32(bars + s));
+    const uint32_t bar = smem_u32(bars + s);
+    const bool two = kRows == 2 && row + 1 < p.M;
+    mbar_arrive_expect_tx(bar, norm_ask_bytes(rows, row) + (two ? norm_ask_bytes(rows, row + 1) : 0u));
+    norm_ask(rows, row, norm_smem + s * stage_bytes, bar);
+    if (two) norm_ask(rows, row + 1, norm_smem + s * stage_bytes + half, bar);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(bars + s), 1);
     mbar_fence_init();
     for (int s = 0; s < stages; ++s) ask(s, blockIdx.x + static_cast<long long>(s) * gridDim.x);
   }
-  // the thread's weights: kept, or read (from L1) for each row before its second sum
-  constexpr bool kKeep = !kLong;
+  constexpr bool kKeep = kRows == 2;
   const bool full = static_cast<int>(blockDim.x) * kEpt == p.H;  // every thread has 16 values
   Held<WT, V> gamma, beta;
   if (kKeep) {
     take_weights<WT, V>(p.gamma, p.H, 1.0f, gamma);
     take_weights<WT, V>(p.beta, p.H, 0.0f, beta);
   }
+  // a sum of each row
+  auto sums = [&](const float (&v)[kRows], float (&out)[kRows], int flip) {
+    if constexpr (kRows == 2) {
+      const float2 s = row_sum2(make_float2(v[0], v[1]), slot, flip);
+      out[0] = s.x * inv;
+      out[1] = s.y * inv;
+    } else {
+      out[0] = row_sum(v[0], reinterpret_cast<float*>(slot), flip) * inv;
+    }
+  };
   __syncthreads();
   int stage = 0;
   uint32_t phase = 0;
-  for (long long row = blockIdx.x; row < p.M; row += gridDim.x) {
+  for (long long turn = blockIdx.x; turn * kRows < p.M; turn += gridDim.x) {
     uint8_t* place = norm_smem + stage * stage_bytes;
-    mbar_wait_drain(smem_u32(bars + stage), phase);
-    if (V * sizeof(T) < 16 && (row == 0 || row == p.M - 1)) {
-      norm_edges<T>(rows, row, place);
+    const long long row = turn * kRows;
+    const int here = p.M - row < kRows ? 1 : kRows;
+    norm_wait(smem_u32(bars + stage), phase);
+    if (V * sizeof(T) < 16 && (row == 0 || row + kRows >= p.M)) {
+      for (int r = 0; r < here; ++r)
+        if (row + r == 0 || row + r == p.M - 1) norm_edges<T>(rows, row + r, place + r * half);
       __syncthreads();
     }
-    const uint8_t* at = rows.base + row * rows.ld;
-    const T* in = reinterpret_cast<const T*>(place + (at - down16(at)));
-    Pair x[NP];
-    {
-      Held<T, V> held;
-      take<T, V>(in, p.H, 0.0f, held);
+    Pair x[kRows][NP];
+    float part[kRows], mean[kRows], rstd[kRows];
 #pragma unroll
-      for (int k = 0; k < NP; ++k) x[k] = pair_at(held, k);
+    for (int r = 0; r < kRows; ++r) {
+      const uint8_t* at = rows.base + (row + (r < here ? r : 0)) * rows.ld;
+      Held<T, V> held;
+      take<T, V>(reinterpret_cast<const T*>(place + (r < here ? r * half : 0) + (at - down16(at))), p.H, 0.0f, held);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) x[r][k] = pair_at(held, k);
+      part[r] = sum_of(x[r]);
     }
-    const float mean = row_sum(sum_of(x), slot, 0) * inv;
+    sums(part, mean, 0);
     __syncwarp();
-    if (threadIdx.x == 0) ask(stage, row + static_cast<long long>(stages) * gridDim.x);
+    if (threadIdx.x == 0) ask(stage, turn + static_cast<long long>(stages) * gridDim.x);
     if (++stage == stages) {
       stage = 0;
       phase ^= 1u;
     }
-    const float q = center<V>(x, mean, p.H, full);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) part[r] = center<V>(x[r], mean[r], p.H, full);
     if (!kKeep) {
       take_weights<WT, V>(p.gamma, p.H, 1.0f, gamma);
       take_weights<WT, V>(p.beta, p.H, 0.0f, beta);
     }
-    const float rstd = rsqrtf(row_sum(q, slot, 1) * inv + p.eps);
-    if (threadIdx.x == 0) {
-      if (p.mean != nullptr) p.mean[row] = mean;
-      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    sums(part, rstd, 1);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) rstd[r] = rsqrtf(rstd[r] + p.eps);
+    if (static_cast<int>(threadIdx.x) < here) {
+      if (p.mean != nullptr) p.mean[row + threadIdx.x] = threadIdx.x == 0 ? mean[0] : mean[kRows - 1];
+      if (p.rstd != nullptr) p.rstd[row + threadIdx.x] = threadIdx.x == 0 ? rstd[0] : rstd[kRows - 1];
     }
-    apply<WT, V>(x, rstd, gamma, beta);
-    put_pairs<T, V>(static_cast<T*>(p.y) + row * p.ldy, p.H, x);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const Pair g = pair_at(gamma, k), b = pair_at(beta, k);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) x[r][k] = fma2(mul2(x[r][k], both(rstd[r])), g, b);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (r < here) put_pairs<T, V>(static_cast<T*>(p.y) + (row + r) * p.ldy, p.H, x[r]);
   }
 }
 
@@ -582,7 +631,7 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const
       rstd_next = __ldg(p.rstd + row + gridDim.x);
     }
     uint8_t* place = norm_smem + stage * stage_bytes;
-    mbar_wait_drain(smem_u32(bars + stage), phase);
+    norm_wait(smem_u32(bars + stage), phase);
     if (V * sizeof(T) < 16 && (row == 0 || row == p.M - 1)) {
       norm_edges<T>(xs, row, place);
       norm_edges<T>(gs, row, place + half);
@@ -703,49 +752,52 @@ int norm_blocks(int M, const dim3& b, int registers) {
 // Bytes of a row's place in the ring: its 16-byte pieces, wherever it begins.
 int norm_place(int size, int H) { return (H * size + 15) / 16 * 16 + 16; }
 
-// The ring's stages for a block with `room` bytes (0: the rows are too short; a
-// copy costs about as long as 1 KB takes, so short rows go through registers,
-// several to a block). rows: rows of a stage.
+// The ring's stages for a block with `room` bytes and `rows` rows a stage.
 int norm_ring_stages(int size, int H, int room, int rows) {
-  if (H * size < 2048) return 0;
   const int n = room / (rows * norm_place(size, H));
   return n < kNormStages ? n : kNormStages;
 }
 
+// Launches a ring kernel over `turns` turns of `rows` places, with at most `most` blocks
+// an SM: as many as the registers allow, so that one's sums run under another's
+// stores. `grid` receives the blocks; 0: the rows are too short for it.
 template <void (*kernel)(const NormLaunch, int, int)>
-cudaError_t norm_ring_launch(const NormLaunch& L, int grid, int threads, int stages, int rows,
+cudaError_t norm_ring_launch(const NormLaunch& L, long long turns, int threads, int rows, int most, int* grid,
                              cudaStream_t stream) {
-  static bool set[64] = {};  // the attribute holds for the process: once per device and kernel
+  static int registers[64] = {};  // of the kernel; its attribute is set: once per device and kernel
+  *grid = 0;
+  const int size = L.x_f32 ? 4 : 2;
+  if (L.H * size < 2048) return cudaSuccess;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!set[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+  if (registers[dev] == 0) {
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, kernel);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
     if (e != cudaSuccess) return e;
-    set[dev] = true;
+    registers[dev] = (a.numRegs + 7) / 8 * 8;
   }
-  const int stage = rows * norm_place(L.x_f32 ? 4 : 2, L.H);
-  kernel<<<grid, threads, static_cast<size_t>(stages) * stage, stream>>>(L, stages, stage);
+  int per_sm = 65536 / (registers[dev] * threads);
+  per_sm = per_sm < 1 ? 1 : per_sm > most ? most : per_sm;
+  const int stages = norm_ring_stages(size, L.H, 200 * 1024 / per_sm, rows);
+  const long long all = static_cast<long long>(device_sm_count()) * per_sm;
+  *grid = static_cast<int>(turns < all ? turns : all);
+  const int stage = rows * norm_place(size, L.H);
+  kernel<<<*grid, threads, static_cast<size_t>(stages) * stage, stream>>>(L, stages, stage);
   return cudaGetLastError();
 }
 
 template <typename T, typename WT, int V>
 cudaError_t norm_forward_launch(const NormLaunch& L, cudaStream_t stream) {
   const dim3 b = norm_block(L.H);
-  const bool is_long = b.x > 512;
-  // blocks an SM: as many as the registers allow, so that one's sums run under another's stores
-  const int regs = is_long || kNormSlim<T, WT, V> ? 64 : 128;
-  const int per_sm = 65536 / (regs * static_cast<int>(b.x)) > 1 ? 65536 / (regs * static_cast<int>(b.x)) : 1;
-  const int ring_blocks = per_sm < 8 ? per_sm : 8;
-  const int stages = norm_ring_stages(sizeof(T), L.H, 200 * 1024 / ring_blocks, 1);
-  if (stages >= 2) {
-    const long long most = static_cast<long long>(device_sm_count()) * ring_blocks;
-    const int grid = static_cast<int>(L.M < most ? L.M : most), threads = static_cast<int>(b.x);
-    return is_long
-               ? norm_ring_launch<norm_ring_kernel<T, WT, V, true>>(L, grid, threads, stages, 1, stream)
-               : norm_ring_launch<norm_ring_kernel<T, WT, V, false>>(L, grid, threads, stages, 1, stream);
-  }
+  const int threads = static_cast<int>(b.x);
+  int grid = 0;
+  const cudaError_t e = b.x > 512 ? norm_ring_launch<norm_ring_kernel<T, WT, V, 1>>(L, L.M, threads, 1, 8, &grid, stream)
+                                  : norm_ring_launch<norm_ring_kernel<T, WT, V, 2>>(L, (L.M + 1ll) / 2, threads, 2, 8,
+                                                                                   &grid, stream);
+  if (e != cudaSuccess || grid > 0) return e;
   norm_kernel<T, WT, V><<<static_cast<unsigned>(norm_blocks(L.M, b, 85)), b, 0, stream>>>(L);
   return cudaGetLastError();
 }
@@ -756,14 +808,9 @@ constexpr int kNormRingBlocks = 4;  // blocks an SM in the backward pass, at mos
 template <typename T, typename WT, int V>
 cudaError_t norm_backward_launch(const NormLaunch& L, int* lines, cudaStream_t stream) {
   const dim3 b = norm_block(L.H);
-  const int per_sm = 65536 / (128 * static_cast<int>(b.x)) > 1 ? 65536 / (128 * static_cast<int>(b.x)) : 1;
-  const int ring_blocks = per_sm < kNormRingBlocks ? per_sm : kNormRingBlocks;
-  const int stages = norm_ring_stages(sizeof(T), L.H, 200 * 1024 / ring_blocks, 2);
-  if (stages >= 2) {
-    const long long most = static_cast<long long>(device_sm_count()) * ring_blocks;
-    *lines = static_cast<int>(L.M < most ? L.M : most);
-    return norm_ring_launch<norm_bwd_ring_kernel<T, WT, V>>(L, *lines, static_cast<int>(b.x), stages, 2, stream);
-  }
+  const cudaError_t e = norm_ring_launch<norm_bwd_ring_kernel<T, WT, V>>(L, L.M, static_cast<int>(b.x), 2,
+                                                                         kNormRingBlocks, lines, stream);
+  if (e != cudaSuccess || *lines > 0) return e;
   const unsigned grid = static_cast<unsigned>(norm_blocks(L.M, b, 128));
   *lines = static_cast<int>(grid);
   norm_bwd_kernel<T, WT, V><<<grid, b, 0, stream>>>(L);
