@@ -499,10 +499,20 @@ class FeedForwardBlock:
                                        routed.ws_gate_up, routed.ws_down)
 
     def forward(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        """out bf16 [T, H] from x bf16 [T, H] (dense rows one after the other)."""
         hidden = self.norm.forward(x)
         logits = self.router.forward(hidden)
         if self.few is not None and x.shape[0] <= MOE_FEW_MAX_TOKENS:
             return self.few.forward(hidden, logits=logits, residual=x, out=out)
-        ids, weights = self.routed.route(logits)
-        routed = self.routed.forward(hidden, ids, weights)
-        return torch.add(x, routed, out=out)
+        e = self.routed
+        prob = e.problem(x.shape[0])
+        with _on_device_of(x):
+            ids, weights = e.route(logits)
+            routed = torch.empty_like(hidden)
+            # a workspace for this call alone (RoutedExperts keeps one for all of its own):
+            # calls on several streams and in several captured graphs do not share it
+            ws = torch.empty(max(moe_workspace_bytes(prob), 1024), dtype=torch.uint8,
+                             device=x.device)
+            moe_experts_forward(prob, hidden, ids, weights, e.w_gate_up, e.w_down,
+                                e.w_down_scales, e.ws_gate_up, e.ws_down, e.scale, routed, ws)
+            return torch.add(x, routed, out=out)

@@ -62,6 +62,50 @@ def test_block_in_a_graph():
     assert torch.equal(out, want)
 
 
+def test_block_of_no_tokens():
+    block, n = make()
+    assert block.forward(n(0, 512)).shape == (0, 512)
+
+
+def test_block_graphs_of_two_sizes():
+    """A graph keeps its workspace while larger calls, captured or not, come and go."""
+    block, n = make()
+    xs = {T: n(T, 512) for T in (80, 300)}
+    want = {T: block.forward(x) for T, x in xs.items()}
+    graphs, outs = {}, {}
+    for T in (80, 300):
+        block.forward(xs[T])
+        torch.cuda.synchronize()
+        graphs[T] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[T]):
+            outs[T] = block.forward(xs[T])
+    big = block.forward(n(900, 512))
+    kept = [torch.full((1 << 20,), 7, dtype=torch.int32, device=DEV) for _ in range(16)]
+    before = big.clone()
+    for T in (80, 300, 80):
+        graphs[T].replay()
+    torch.cuda.synchronize()
+    for T in (80, 300):
+        assert torch.equal(outs[T], want[T])
+    assert torch.equal(big, before) and all(bool((k == 7).all()) for k in kept)
+
+
+def test_block_on_two_streams():
+    block, n = make()
+    xs = [n(200, 512) for _ in range(2)]
+    want = [block.forward(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(block.forward(xs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
 def test_block_checks():
     block, n = make()
     with pytest.raises(ValueError):
