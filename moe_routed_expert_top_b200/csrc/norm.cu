@@ -416,13 +416,35 @@ __device__ __forceinline__ NormRows norm_rows(const void* x, long long ld, int M
   return r;
 }
 
-// The 16-byte pieces of a row that lie in the matrix: [lo, hi).
-__device__ __forceinline__ void norm_span(const NormRows& r, long long row, const uint8_t*& lo, const uint8_t*& hi) {
+// The 16-byte pieces of a row that lie in the matrix, [lo, hi), and how far into the
+// row's place the first belongs. kWhole: rows begin and end at pieces (one thread asks
+// for all rows while the others work, so its instructions count).
+struct NormSpan {
+  const uint8_t *lo, *hi;
+  uint32_t into;
+};
+template <bool kWhole>
+__device__ __forceinline__ NormSpan norm_span(const NormRows& r, long long row) {
   const uint8_t* at = r.base + row * r.ld;
-  lo = down16(at);
-  hi = up16(at + r.bytes);
-  if (lo < r.base) lo = up16(r.base);
-  if (hi > r.end) hi = down16(r.end);
+  NormSpan s{at, at + r.bytes, 0u};
+  if (!kWhole) {
+    s.lo = down16(at);
+    s.hi = up16(s.hi);
+    if (s.lo < r.base) s.lo = up16(r.base);
+    if (s.hi > r.end) s.hi = down16(r.end);
+    s.into = static_cast<uint32_t>(s.lo - down16(at));
+  }
+  return s;
+}
+__device__ __forceinline__ uint32_t norm_bytes(const NormSpan& s) { return static_cast<uint32_t>(s.hi - s.lo); }
+
+// Asks for a row. Its place in `dst` (16-byte aligned) begins at its address's offset
+// from a 16-byte piece.
+__device__ __forceinline__ void norm_ask(const NormSpan& s, uint8_t* dst, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst) + s.into),
+               "l"(s.lo), "r"(norm_bytes(s)), "r"(bar)
+               : "memory");
 }
 
 // A row's arrival. (Most have arrived: the bounded wait reads the time first, which
@@ -431,29 +453,12 @@ __device__ __forceinline__ void norm_wait(uint32_t bar, uint32_t phase) {
   if (!mbar_try_wait(bar, phase)) mbar_wait_drain(bar, phase);
 }
 
-// Asks for a row (one thread). The row's place in `dst` (16-byte aligned) begins at
-// its address's offset from a 16-byte piece.
-__device__ __forceinline__ uint32_t norm_ask_bytes(const NormRows& r, long long row) {
-  const uint8_t *lo, *hi;
-  norm_span(r, row, lo, hi);
-  return static_cast<uint32_t>(hi - lo);
-}
-__device__ __forceinline__ void norm_ask(const NormRows& r, long long row, uint8_t* dst, uint32_t bar) {
-  const uint8_t *lo, *hi;
-  norm_span(r, row, lo, hi);
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst) + static_cast<uint32_t>(lo - down16(r.base + row * r.ld))),
-               "l"(lo), "r"(static_cast<uint32_t>(hi - lo)), "r"(bar)
-               : "memory");
-}
-
 // The values of the first and last row that no copy brings (whole block; a barrier
 // has to follow).
 template <typename T>
 __device__ __forceinline__ void norm_edges(const NormRows& r, long long row, uint8_t* dst) {
-  const uint8_t *lo, *hi;
-  norm_span(r, row, lo, hi);
-  const uint8_t* at = r.base + row * r.ld;
+  const NormSpan s = norm_span<false>(r, row);
+  const uint8_t *lo = s.lo, *hi = s.hi, *at = r.base + row * r.ld;
   const int n = r.bytes / static_cast<int>(sizeof(T));
   const int head = lo > at ? static_cast<int>((lo - at) / sizeof(T)) : 0;
   const int tail = hi < at + r.bytes ? static_cast<int>((at + r.bytes - hi) / sizeof(T)) : 0;
@@ -465,13 +470,14 @@ __device__ __forceinline__ void norm_edges(const NormRows& r, long long row, uin
 
 // A block takes kRows neighbouring rows a turn: with two, one barrier and half the
 // shuffles serve both rows' sums, and the weights are widened once for both (16384 x
-// 2048 bf16: 35 us with one, 28 us with two). Rows of more than 8192 values, whose
+// 2048 bf16: 35 us with one, 26 us with two). Rows of more than 8192 values, whose
 // 1024 threads have 64 registers each, come one by one, and their weights are read
 // (from L1) for each; else a thread keeps its weights.
 template <typename T, typename WT, int V, int kRows>
 __global__ void __launch_bounds__(kRows == 1 ? 1024 : 512) norm_ring_kernel(const NormLaunch p, int stages,
                                                                            int stage_bytes) {
   constexpr int NP = kEpt / 2;
+  constexpr bool kWhole = V * sizeof(T) == 16;
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ float2 slot[2 * 32];
   __shared__ uint64_t bars[kNormStages];
@@ -483,9 +489,10 @@ __global__ void __launch_bounds__(kRows == 1 ? 1024 : 512) norm_ring_kernel(cons
     if (row >= p.M) return;
     const uint32_t bar = smem_u32(bars + s);
     const bool two = kRows == 2 && row + 1 < p.M;
-    mbar_arrive_expect_tx(bar, norm_ask_bytes(rows, row) + (two ? norm_ask_bytes(rows, row + 1) : 0u));
-    norm_ask(rows, row, norm_smem + s * stage_bytes, bar);
-    if (two) norm_ask(rows, row + 1, norm_smem + s * stage_bytes + half, bar);
+    const NormSpan first = norm_span<kWhole>(rows, row), second = norm_span<kWhole>(rows, two ? row + 1 : row);
+    mbar_arrive_expect_tx(bar, norm_bytes(first) + (two ? norm_bytes(second) : 0u));
+    norm_ask(first, norm_smem + s * stage_bytes, bar);
+    if (two) norm_ask(second, norm_smem + s * stage_bytes + half, bar);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(bars + s), 1);
@@ -517,7 +524,7 @@ __global__ void __launch_bounds__(kRows == 1 ? 1024 : 512) norm_ring_kernel(cons
     const long long row = turn * kRows;
     const int here = p.M - row < kRows ? 1 : kRows;
     norm_wait(smem_u32(bars + stage), phase);
-    if (V * sizeof(T) < 16 && (row == 0 || row + kRows >= p.M)) {
+    if (!kWhole && (row == 0 || row + kRows >= p.M)) {
       for (int r = 0; r < here; ++r)
         if (row + r == 0 || row + r == p.M - 1) norm_edges<T>(rows, row + r, place + r * half);
       __syncthreads();
@@ -596,6 +603,7 @@ template <typename T, typename WT, int V>
 __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const NormLaunch p, int stages,
                                                                            int stage_bytes) {
   constexpr int NP = kEpt / 2;
+  constexpr bool kWhole = V * sizeof(T) == 16;
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ float2 slot[2 * 32];
   __shared__ uint64_t bars[kNormStages];
@@ -606,9 +614,10 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const
   auto ask = [&](int s, long long row) {
     if (row >= p.M) return;
     const uint32_t bar = smem_u32(bars + s);
-    mbar_arrive_expect_tx(bar, norm_ask_bytes(xs, row) + norm_ask_bytes(gs, row));
-    norm_ask(xs, row, norm_smem + s * stage_bytes, bar);
-    norm_ask(gs, row, norm_smem + s * stage_bytes + half, bar);
+    const NormSpan sx = norm_span<kWhole>(xs, row), sg = norm_span<kWhole>(gs, row);
+    mbar_arrive_expect_tx(bar, norm_bytes(sx) + norm_bytes(sg));
+    norm_ask(sx, norm_smem + s * stage_bytes, bar);
+    norm_ask(sg, norm_smem + s * stage_bytes + half, bar);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(bars + s), 1);
@@ -632,7 +641,7 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_ring_kernel(const
     }
     uint8_t* place = norm_smem + stage * stage_bytes;
     norm_wait(smem_u32(bars + stage), phase);
-    if (V * sizeof(T) < 16 && (row == 0 || row == p.M - 1)) {
+    if (!kWhole && (row == 0 || row == p.M - 1)) {
       norm_edges<T>(xs, row, place);
       norm_edges<T>(gs, row, place + half);
       __syncthreads();
