@@ -39,6 +39,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <climits>
 #include <cstring>
 #include <mutex>
 #include <type_traits>
@@ -69,15 +70,19 @@ static_assert(kLinSmem <= 227 * 1024, "shared memory");
 struct LinProblem {
   int M, N;
   int a_mn, b_mn;
-  int a_3d, b_3d;          // the operand's stage is one copy (3-D tensor map)
+  int a_whole, b_whole;    // see lin_load
   int swap;                // the tile's rows are y's columns (few rows of x: see lin_swapped)
   int bn;                  // tile width: a multiple of 32, at most kMaxBn
   int tiles_m, tiles_n;
   int splits;              // parts of each tile, along k
   int kb_total, kb_split;  // k blocks of 128: all, and of one part
   float* partial;          // [splits][tiles][256][bn] sums of the parts (swap: [bn][256])
-  int wide;                // every row of y, z and residual takes 32-byte accesses
+  int wide;                // every row of y, z and residual takes accesses of 32 bytes (2), of 16 (1)
   LinearEpilogue e;
+};
+// Tensor maps: A and B of each product, as blocks of 64 and as they are.
+struct LinMaps {
+  CUtensorMap three[4], two[4];
 };
 struct LinParams {
   LinProblem p[2];
@@ -140,44 +145,59 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t smem_dst, const void* 
 }
 
 // One operand's part of a stage: `rows` output indices from o0 on x 128 k from k0 on.
-__device__ __forceinline__ void lin_load(uint32_t dst, const CUtensorMap* tm, bool mn, bool three, int o0, int rows,
-                                         int k0, uint32_t bar, uint64_t pol) {
-  if (three) {
+// whole: the inner index's whole blocks of 64, in elements (0: 2-D copies alone).
+__device__ __forceinline__ void lin_load(uint32_t dst, const CUtensorMap* three, const CUtensorMap* two, bool mn,
+                                         int whole, int o0, int rows, int k0, uint32_t bar, uint64_t pol) {
+  if ((mn ? o0 + rows : k0 + kBk) <= whole) {
     if (mn)
-      tma_load_3d_pair(dst, tm, k0, o0 / 64, bar, pol);
+      tma_load_3d_pair(dst, three, k0, o0 / 64, bar, pol);
     else
-      tma_load_3d_pair(dst, tm, o0, k0 / 64, bar, pol);
+      tma_load_3d_pair(dst, three, o0, k0 / 64, bar, pol);
   } else if (mn) {
-    tma_load_2d_pair(dst, tm, o0, k0, bar, pol);
-    if (rows > 64) tma_load_2d_pair(dst + kBk * 128, tm, o0 + 64, k0, bar, pol);
+    tma_load_2d_pair(dst, two, o0, k0, bar, pol);
+    if (rows > 64) tma_load_2d_pair(dst + kBk * 128, two, o0 + 64, k0, bar, pol);
   } else {
-    tma_load_2d_pair(dst, tm, k0, o0, bar, pol);
-    tma_load_2d_pair(dst + rows * 128, tm, k0 + 64, o0, bar, pol);
+    tma_load_2d_pair(dst, two, k0, o0, bar, pol);
+    tma_load_2d_pair(dst + rows * 128, two, k0 + 64, o0, bar, pol);
   }
 }
 
-__device__ __forceinline__ void lin_st8(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+// 32 bytes, in one access or (w32 false) two.
+__device__ __forceinline__ void lin_st8(void* p, const uint32_t* v, bool w32) {
+  if (w32) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
-__device__ __forceinline__ void lin_ld8(uint32_t* v, const void* p) {
-  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(p));
-}
-__device__ __forceinline__ void lin_store32_f32(float* dst, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void lin_ld8(uint32_t* v, const void* p, bool w32) {
+  if (w32) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+  } else {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) lin_st8(dst + i, v + i);
+    for (int i = 0; i < 2; ++i)
+      asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v[4 * i]), "=r"(v[4 * i + 1]), "=r"(v[4 * i + 2]), "=r"(v[4 * i + 3])
+                   : "l"(static_cast<const uint8_t*>(p) + 16 * i));
+  }
 }
-__device__ __forceinline__ void lin_store32_bf16(__nv_bfloat16* dst, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void lin_store32_f32(float* dst, const uint32_t (&v)[32], bool w32) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) lin_st8(dst + i, v + i, w32);
+}
+__device__ __forceinline__ void lin_store32_bf16(__nv_bfloat16* dst, const uint32_t (&v)[32], bool w32) {
 #pragma unroll
   for (int i = 0; i < 32; i += 16) {
     uint32_t o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       o[j] = pack_bf16x2(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
-    lin_st8(dst + i, o);
+    lin_st8(dst + i, o, w32);
   }
 }
 
@@ -187,53 +207,189 @@ __device__ __forceinline__ void lin_act32(uint32_t (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(linear_act(__uint_as_float(v[i]), kAct));
 }
 
-// The epilogue of 32 columns n.. of row m, all accesses 32 bytes wide. v: the sums
+__device__ __forceinline__ void lin_act32_of(int act, uint32_t (&v)[32]) {
+  if (act == kActRelu)
+    lin_act32<kActRelu>(v);
+  else if (act == kActSilu)
+    lin_act32<kActSilu>(v);
+  else if (act == kActGelu)
+    lin_act32<kActGelu>(v);
+}
+// v += 32 bf16 residual values, in pairs
+__device__ __forceinline__ void lin_add_res(uint32_t (&v)[32], const uint32_t (&res)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[2 * i] = __float_as_uint(__uint_as_float(v[2 * i]) + bf16lo_to_f32(res[i]));
+    v[2 * i + 1] = __float_as_uint(__uint_as_float(v[2 * i + 1]) + bf16hi_to_f32(res[i]));
+  }
+}
+
+// The epilogue of 32 columns n.. of row m, by wide accesses of one thread. v: the sums
 // with their bias; res: the residual's values if they are bf16.
 __device__ __forceinline__ void lin_store32(const LinearEpilogue& e, long long m, int n, uint32_t (&v)[32],
-                                            const uint32_t (&res)[16]) {
-  if (e.z != nullptr) lin_store32_bf16(static_cast<__nv_bfloat16*>(e.z) + m * e.ldz + n, v);
-  if (e.act == kActRelu)
-    lin_act32<kActRelu>(v);
-  else if (e.act == kActSilu)
-    lin_act32<kActSilu>(v);
-  else if (e.act == kActGelu)
-    lin_act32<kActGelu>(v);
+                                            const uint32_t (&res)[16], bool w32) {
+  if (e.z != nullptr) lin_store32_bf16(static_cast<__nv_bfloat16*>(e.z) + m * e.ldz + n, v, w32);
+  lin_act32_of(e.act, v);
   if (e.res != nullptr) {
     if (e.res_f32) {
       const float* src = static_cast<const float*>(e.res) + m * e.ldr + n;
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
         uint32_t r[8];
-        lin_ld8(r, src + i);
+        lin_ld8(r, src + i, w32);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           v[i + j] = __float_as_uint(__uint_as_float(v[i + j]) + __uint_as_float(r[j]));
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        v[2 * i] = __float_as_uint(__uint_as_float(v[2 * i]) + bf16lo_to_f32(res[i]));
-        v[2 * i + 1] = __float_as_uint(__uint_as_float(v[2 * i + 1]) + bf16hi_to_f32(res[i]));
-      }
+      lin_add_res(v, res);
     }
   }
   if (e.y_f32)
-    lin_store32_f32(static_cast<float*>(e.y) + m * e.ldy + n, v);
+    lin_store32_f32(static_cast<float*>(e.y) + m * e.ldy + n, v, w32);
   else
-    lin_store32_bf16(static_cast<__nv_bfloat16*>(e.y) + m * e.ldy + n, v);
+    lin_store32_bf16(static_cast<__nv_bfloat16*>(e.y) + m * e.ldy + n, v, w32);
 }
 
-// 32 bf16 residual values of row m from n on, 32 bytes wide (res_f32: not taken).
-__device__ __forceinline__ void lin_fetch_res(const LinearEpilogue& e, long long m, int n, uint32_t (&r)[16]) {
+// 32 bf16 residual values of row m from n on, by wide accesses.
+__device__ __forceinline__ void lin_fetch_res(const LinearEpilogue& e, long long m, int n, uint32_t (&r)[16], bool w32) {
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.res) + m * e.ldr + n;
-  lin_ld8(r, src);
-  lin_ld8(r + 8, src + 16);
+  lin_ld8(r, src, w32);
+  lin_ld8(r + 8, src + 16, w32);
+}
+
+// ---- The same for rows at any address (odd pitches, a tile's last columns). A warp's
+// block of 32 rows x `cols` columns goes through shared memory (17 words a row), so
+// that 16 lanes lie along a row: a lane has the columns s + 2w and s + 2w + 1, where s
+// is 1 in a row that begins between two words; in such a row lane 15 has the last
+// column and the first.
+struct LinLane {
+  int c0, c1;  // the lane's columns; whether they are one word
+  bool word;
+};
+__device__ __forceinline__ LinLane lin_lane(const __nv_bfloat16* row, int cols) {
+  const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1) & 1, w = threadIdx.x & 15;
+  LinLane l;
+  l.c0 = s + 2 * w;
+  l.c1 = s + 2 * w + 1 > 31 ? 0 : l.c0 + 1;
+  l.word = l.c1 != 0 && l.c1 < cols;
+  return l;
+}
+// The lane's words of the block's rows 0 1, 2 3, ... (rows: `ld` apart from row0 on)
+__device__ __forceinline__ void lin_fetch_rows(const __nv_bfloat16* row0, long long ld, int rows, int cols,
+                                               uint32_t (&r)[16]) {
+  const __nv_bfloat16* row = row0 + ((threadIdx.x & 31) >> 4) * ld;
+#pragma unroll
+  for (int i = 0; i < 16; ++i, row += 2 * ld) {
+    r[i] = 0u;
+    if (2 * i + static_cast<int>((threadIdx.x & 31) >> 4) >= rows) continue;
+    const LinLane l = lin_lane(row, cols);
+    if (l.word) {
+      r[i] = *reinterpret_cast<const uint32_t*>(row + l.c0);
+    } else {
+      const uint16_t* at = reinterpret_cast<const uint16_t*>(row);
+      if (l.c0 < cols) r[i] = at[l.c0];
+      if (l.c1 < cols) r[i] |= static_cast<uint32_t>(at[l.c1]) << 16;
+    }
+  }
+}
+// v += the residual's block that lin_fetch_rows brought (a thread's v: its row's columns)
+__device__ __forceinline__ void lin_add_rows(const __nv_bfloat16* row0, long long ld, int cols, const uint32_t (&r)[16],
+                                             float* block, uint32_t (&v)[32]) {
+  uint16_t* b = reinterpret_cast<uint16_t*>(block);
+  const int up = (threadIdx.x & 31) >> 4;
+  const __nv_bfloat16* row = row0 + up * ld;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i, row += 2 * ld) {
+    const LinLane l = lin_lane(row, cols);
+    b[(2 * i + up) * 34 + l.c0] = static_cast<uint16_t>(r[i]);
+    if (l.c1 < cols) b[(2 * i + up) * 34 + l.c1] = static_cast<uint16_t>(r[i] >> 16);
+  }
+  __syncwarp();
+  uint32_t mine[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) mine[i] = reinterpret_cast<const uint32_t*>(block)[(threadIdx.x & 31) * 17 + i];
+  lin_add_res(v, mine);
+}
+// Rounds and stores the block (a thread's v: its row's columns).
+__device__ __forceinline__ void lin_put_rows(__nv_bfloat16* row0, long long ld, int rows, int cols,
+                                             const uint32_t (&v)[32], float* block) {
+  uint16_t* b = reinterpret_cast<uint16_t*>(block);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    reinterpret_cast<uint32_t*>(block)[(threadIdx.x & 31) * 17 + i] =
+        pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+  __syncwarp();
+  const int up = (threadIdx.x & 31) >> 4;
+  __nv_bfloat16* row = row0 + up * ld;
+#pragma unroll 4
+  for (int r = up; r < rows; r += 2, row += 2 * ld) {
+    const LinLane l = lin_lane(row, cols);
+    const uint16_t lo = b[r * 34 + l.c0], hi = b[r * 34 + l.c1];
+    if (l.word) {
+      *reinterpret_cast<uint32_t*>(row + l.c0) = lo | static_cast<uint32_t>(hi) << 16;
+    } else {
+      uint16_t* at = reinterpret_cast<uint16_t*>(row);
+      if (l.c0 < cols) at[l.c0] = lo;
+      if (l.c1 < cols) at[l.c1] = hi;
+    }
+  }
+}
+// fp32 rows: 16 columns at a time, a half warp along a row. kAdd: v += the block;
+// else the block = v.
+template <bool kAdd>
+__device__ __forceinline__ void lin_rows_f32(float* row0, long long ld, int rows, int cols, uint32_t (&v)[32],
+                                             float* block) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    __syncwarp();
+    if (!kAdd) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) block[lane * 17 + i] = __uint_as_float(v[16 * half + i]);
+      __syncwarp();
+    }
+    if (16 * half + c < cols) {
+      float* at = row0 + (lane >> 4) * ld + 16 * half + c;
+#pragma unroll 8
+      for (int r = lane >> 4; r < rows; r += 2, at += 2 * ld) {
+        if (kAdd)
+          block[r * 17 + c] = *at;
+        else
+          *at = block[r * 17 + c];
+      }
+    }
+    if (kAdd) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[16 * half + i] = __float_as_uint(__uint_as_float(v[16 * half + i]) + block[lane * 17 + i]);
+    }
+  }
+}
+// The epilogue of a block; `res` as lin_fetch_rows brought it.
+__device__ __forceinline__ void lin_store_rows(const LinearEpilogue& e, long long m, int n, int rows, int cols,
+                                               uint32_t (&v)[32], const uint32_t (&res)[16], float* block) {
+  if (e.z != nullptr)
+    lin_put_rows(static_cast<__nv_bfloat16*>(e.z) + m * e.ldz + n, e.ldz, rows, cols, v, block);
+  lin_act32_of(e.act, v);
+  if (e.res != nullptr) {
+    if (e.res_f32)
+      lin_rows_f32<true>(const_cast<float*>(static_cast<const float*>(e.res)) + m * e.ldr + n, e.ldr, rows, cols, v,
+                         block);
+    else
+      lin_add_rows(static_cast<const __nv_bfloat16*>(e.res) + m * e.ldr + n, e.ldr, cols, res, block, v);
+  }
+  if (e.y_f32)
+    lin_rows_f32<false>(static_cast<float*>(e.y) + m * e.ldy + n, e.ldy, rows, cols, v, block);
+  else
+    lin_put_rows(static_cast<__nv_bfloat16*>(e.y) + m * e.ldy + n, e.ldy, rows, cols, v, block);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
-    linear_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
-                       const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
-                       const __grid_constant__ LinParams args) {
+    linear_gemm_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinParams args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -269,12 +425,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     mbar_fence_init();
-    tma_prefetch_desc(&tmA0);
-    tma_prefetch_desc(&tmB0);
-    if (args.end[1] > args.end[0]) {
-      tma_prefetch_desc(&tmA1);
-      tma_prefetch_desc(&tmB1);
-    }
+    for (int i = 0; i < (args.end[1] > args.end[0] ? 4 : 2); ++i)
+      tma_prefetch_desc(i & 1 ? (args.p[i >> 1].b_whole > 0 ? &maps.three[i] : &maps.two[i])
+                              : (args.p[i >> 1].a_whole > 0 ? &maps.three[i] : &maps.two[i]));
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), kNumAcc * kMaxBn);
   // what follows reads what earlier kernels of the stream wrote
@@ -298,13 +451,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       for (int t = pair; ok && t < args.end[1]; t += npairs) {
         const LinItem it = lin_item(args, t);
         const LinProblem& p = args.p[it.which];
-        const CUtensorMap* tmA = it.which ? &tmA1 : &tmA0;
-        const CUtensorMap* tmB = it.which ? &tmB1 : &tmB0;
+        const CUtensorMap* three = maps.three + 2 * it.which;
+        const CUtensorMap* two = maps.two + 2 * it.which;
         const int half = p.bn / 2;
         const int m0 = it.tm * 256 + static_cast<int>(rank) * 128;
         const int n0 = it.tn * p.bn + static_cast<int>(rank) * half;
         const uint32_t bytes = kStageA + (p.b_mn ? (half + 63) / 64 * kBk * 128 : half * kBk * 2);
-        const bool a_mn = p.a_mn, b_mn = p.b_mn, a_3d = p.a_3d, b_3d = p.b_3d;
+        const bool a_mn = p.a_mn, b_mn = p.b_mn;
+        const int a_whole = p.a_whole, b_whole = p.b_whole;
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, status)) {
             ok = false;
@@ -315,8 +469,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           if (leader) mbar_arrive_expect_tx(fb_local, 2u * bytes);
           const uint32_t a_dst = smem_u32(smem) + stage * stage_bytes;
           const uint32_t b_dst = a_dst + kStageA;
-          lin_load(a_dst, tmA, a_mn, a_3d, m0, 128, kb * kBk, fb, pol);
-          lin_load(b_dst, tmB, b_mn, b_3d, n0, half, kb * kBk, fb, pol);
+          lin_load(a_dst, three, two, a_mn, a_whole, m0, 128, kb * kBk, fb, pol);
+          lin_load(b_dst, three + 1, two + 1, b_mn, b_whole, n0, half, kb * kBk, fb, pol);
           ++issued;
           if (++stage == stages) {
             stage = 0;
@@ -410,11 +564,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     // A tile's columns go in runs of 32, the even ones to group 0 and the odd
     // ones to group 1; a warp has 32 rows. Tensor memory gives a thread 32
     // columns of one row.
-    //   32-byte accesses possible: it stores them as they are (32 rows at a time,
-    //     whole sectors), the residual's next run already on its way;
+    //   16-byte accesses possible: it stores them as they are (32 rows at a time);
     //   else (odd pitches, the last columns): through shared memory, so that the
     //     lanes lie along the row (a 2-byte store to 32 rows at a time would cost
     //     more than the main loop).
+    // The residual's next run is already on its way either way.
     const int grp = (warp - 2) >> 2;
     const int q = warp & 3;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
@@ -432,7 +586,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       const int c0 = it.tn * p.bn;
       const int width = min(p.bn, p.N - c0);
       const bool has_bias = !sums && p.e.bias != nullptr;
-      const bool fetch = !p.swap && !sums && p.wide && p.e.res != nullptr && !p.e.res_f32;
+      const bool w32 = p.wide == 2;
+      const bool fetch = !p.swap && !sums && rows > 0 && p.e.res != nullptr && !p.e.res_f32;
       __syncwarp();
       if (has_bias && !p.swap)
 #pragma unroll
@@ -442,7 +597,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         }
       __syncwarp();
       uint32_t res[16];
-      if (fetch && lane < rows && grp * 32 + 32 <= width) lin_fetch_res(p.e, m0 + lane, c0 + grp * 32, res);
+      auto ask_res = [&](int j) {  // of the run at column j of the tile
+        if (!fetch || j >= width) return;
+        if (p.wide && width - j >= 32) {
+          if (lane < rows) lin_fetch_res(p.e, m0 + lane, c0 + j, res, w32);
+        } else {
+          lin_fetch_rows(static_cast<const __nv_bfloat16*>(p.e.res) + m0 * p.e.ldr + c0 + j, p.e.ldr, rows,
+                         min(32, width - j), res);
+        }
+      };
+      ask_res(grp * 32);
       bool got = true;
       if (lane == 0) got = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, status);
       got = __shfl_sync(0xffffffffu, got, 0);
@@ -468,28 +632,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               const int ny = static_cast<int>(m0) + lane;
               const float bv = linear_bias(p.e, ny);
 #pragma unroll
-              for (int i0 = 0; i0 < 32; i0 += 8) {
-                float r8[8];
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + bv);
+              if (p.e.z != nullptr) {
+                __nv_bfloat16* at = static_cast<__nv_bfloat16*>(p.e.z) + n * p.e.ldz + ny;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  r8[i] = p.e.res != nullptr && i0 + i < cols ? linear_res(p.e, n + i0 + i, ny) : 0.0f;
+                for (int i = 0; i < 32; ++i, at += p.e.ldz)
+                  if (i < cols) *at = __float2bfloat16(__uint_as_float(v[i]));
+              }
+              lin_act32_of(p.e.act, v);
+              if (p.e.res != nullptr) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (i0 + i < cols) {
-                    float z;
-                    const float y = linear_result(p.e, __uint_as_float(v[i0 + i]), bv, r8[i], &z);
-                    linear_put(p.e, n + i0 + i, ny, y, z);
-                  }
+                for (int i0 = 0; i0 < 32; i0 += 16) {
+                  float r16[16];
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) r16[i] = i0 + i < cols ? linear_res(p.e, n + i0 + i, ny) : 0.0f;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) v[i0 + i] = __float_as_uint(__uint_as_float(v[i0 + i]) + r16[i]);
+                }
+              }
+              if (p.e.y_f32) {
+                float* at = static_cast<float*>(p.e.y) + n * p.e.ldy + ny;
+#pragma unroll
+                for (int i = 0; i < 32; ++i, at += p.e.ldy)
+                  if (i < cols) *at = __uint_as_float(v[i]);
+              } else {
+                __nv_bfloat16* at = static_cast<__nv_bfloat16*>(p.e.y) + n * p.e.ldy + ny;
+#pragma unroll
+                for (int i = 0; i < 32; ++i, at += p.e.ldy)
+                  if (i < cols) *at = __float2bfloat16(__uint_as_float(v[i]));
               }
             }
           }
         } else if (sums) {
-          if (lane < rows) lin_store32_f32(it.partial + (r0 + lane) * p.bn + j, v);
-        } else if (p.wide && cols == 32) {
+          if (lane < rows) lin_store32_f32(it.partial + (r0 + lane) * p.bn + j, v, true);
+        } else {
           uint32_t now[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) now[i] = res[i];
-          if (fetch && lane < rows && j + 96 <= width) lin_fetch_res(p.e, m0 + lane, n + 64, res);
+          ask_res(j + 64);
           if (has_bias) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -500,32 +680,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) + bv.w);
             }
           }
-          if (lane < rows) lin_store32(p.e, m0 + lane, n, v, now);
-        } else {
-          const int c = lane & 15;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) block[lane * 17 + i] = __uint_as_float(v[16 * half + i]);
-            __syncwarp();
-            if (16 * half + c < cols) {
-              const int nc = n + 16 * half + c;
-              const float bv = has_bias ? b[16 * half + c] : 0.0f;
-              for (int i0 = lane >> 4; i0 < rows; i0 += 16) {  // a half warp's rows: every second one
-                float r8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  r8[i] = p.e.res != nullptr && i0 + 2 * i < rows ? linear_res(p.e, m0 + i0 + 2 * i, nc) : 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (i0 + 2 * i < rows) {
-                    float z;
-                    const float y = linear_result(p.e, block[(i0 + 2 * i) * 17 + c], bv, r8[i], &z);
-                    linear_put(p.e, m0 + i0 + 2 * i, nc, y, z);
-                  }
-              }
-            }
+          if (p.wide && cols == 32) {
+            if (lane < rows) lin_store32(p.e, m0 + lane, n, v, now, w32);
+          } else {
+            lin_store_rows(p.e, m0, n, rows, cols, v, now, block);
           }
         }
       }
@@ -549,7 +707,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 }
 
 // y of the tiles computed in parts: the parts' sums, in order. A block has 8 rows
-// of one tile, a thread 8 columns of one, and the loads of 4 parts in flight.
+// of one tile, a thread 8 columns of one and the loads of 4 parts in flight. The
+// columns are neighbours where y's rows take 16-byte accesses, else 32 apart, so that
+// the lanes lie along the row.
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinProblem p, int first) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tile = first + blockIdx.y;
@@ -558,15 +718,43 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
   // y's rows and columns of the tile, its pitch in the table and where it begins
   const int height = p.swap ? p.bn : 256, pitch = p.swap ? 256 : p.bn;
   const int M = p.swap ? p.N : p.M, N = p.swap ? p.M : p.N;
-  const int c = threadIdx.x * 8, n = (p.swap ? tm * 256 : tn * p.bn) + c;
+  const int n0 = p.swap ? tm * 256 : tn * p.bn;
   const int row = blockIdx.x * 8 + threadIdx.y;
   const long long m = (p.swap ? static_cast<long long>(tn) * p.bn : static_cast<long long>(tm) * 256) + row;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c >= pitch || row >= height || n >= N || m >= M) return;
+  if (row >= height || m >= M) return;
   const long long step = static_cast<long long>(p.tiles_m) * p.tiles_n * 256 * p.bn;
-  const float* src = p.partial + static_cast<long long>(tile) * 256 * p.bn + row * pitch + c;
+  const float* line = p.partial + static_cast<long long>(tile) * 256 * p.bn + row * pitch;
+  const bool near = p.wide && !p.e.y_f32 && (p.e.res == nullptr || !p.e.res_f32);
+  if (!near) {
+    const int width = min(pitch, N - n0);
+    float s[8] = {};
+    for (int k0 = 0; k0 < p.splits; k0 += 4) {
+      float v[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = threadIdx.x + 32 * j;
+          v[i][j] = k0 + i < p.splits && c < width ? line[(k0 + i) * step + c] : 0.0f;
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += v[i][j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = threadIdx.x + 32 * j;
+      if (c < width) linear_store(p.e, m, n0 + c, s[j]);
+    }
+    return;
+  }
+  const int c = threadIdx.x * 8, n = n0 + c;
+  if (c >= pitch || n >= N) return;
+  const float* src = line + c;
   const int cols = min(8, N - n);
-  const bool fast = p.wide && cols == 8 && !p.e.y_f32 && (p.e.res == nullptr || !p.e.res_f32);
+  const bool fast = cols == 8;
   float bias[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) bias[j] = j < cols ? linear_bias(p.e, n + j) : 0.0f;
@@ -786,8 +974,8 @@ bool lin_encode(CUtensorMap* map, const void* base, uint64_t inner, uint64_t row
 // The same as blocks of 64 inner elements: dims (64, rows, inner / 64), so that one
 // copy brings a whole stage of an operand (a copy costs its issuer about as long
 // as 8 KB take; with four copies of 8 KB a 64-wide step the backward products ran
-// at 0.85 of their speed with one of 16 KB each). Needs inner % 64 == 0: the last
-// block would otherwise read into the next row.
+// at 0.85 of their speed with one of 16 KB each). Whole blocks only: a part of one
+// would read into the next row.
 bool lin_encode3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
                  uint32_t box_blocks, uint64_t ld) {
   auto fn = lin_encode_fn();
@@ -801,14 +989,24 @@ bool lin_encode3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t ro
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// An operand of `out` output indices and K, of which a stage takes `rows` and 128.
-bool lin_operand(CUtensorMap* map, int* three, const void* base, int mn, int out, int K, int rows, long long ld) {
+// An operand of `out` output indices and K, of which a stage takes `rows` and 128:
+// its maps, and where its whole blocks of 64 end (what is past them has to be filled
+// with zeros, not with the next row: 2-D copies).
+bool lin_operand(CUtensorMap* three, CUtensorMap* two, int* whole, const void* base, int mn, int out, int K, int rows,
+                 long long ld) {
   const int inner = mn ? out : K;
-  *three = inner % 64 == 0 && (!mn || rows % 64 == 0);  // (mn: copies start at whole blocks)
-  if (*three)
-    return mn ? lin_encode3(map, base, out, K, kBk, (rows + 63) / 64, ld)
-              : lin_encode3(map, base, K, out, rows, kBk / 64, ld);
-  return mn ? lin_encode(map, base, out, K, kBk, ld) : lin_encode(map, base, K, out, rows, ld);
+  *whole = !mn || rows % 64 == 0 ? inner / 64 * 64 : 0;  // (mn: copies start at whole blocks)
+  if (*whole > 0) {
+    const bool ok = mn ? lin_encode3(three, base, out, K, kBk, (rows + 63) / 64, ld)
+                       : lin_encode3(three, base, K, out, rows, kBk / 64, ld);
+    if (!ok) return false;
+    // whole stages alone (past a whole last block the 3-D copy fills with zeros too)
+    if (inner % 64 == 0) {
+      *whole = INT_MAX;
+      return true;
+    }
+  }
+  return mn ? lin_encode(two, base, out, K, kBk, ld) : lin_encode(two, base, K, out, rows, ld);
 }
 
 // What each product of a launch does: tile width, parts of a tile along k.
@@ -908,17 +1106,23 @@ cudaError_t launch_linear_gemm(const LinearProduct* L, int count, float* partial
   }
   LinPlan plan[2] = {};
   lin_plan(L, count, plan);
-  CUtensorMap tm[4];
+  LinMaps maps = {};
   LinParams args = {};
   args.status = status;
   long long items = 0;
   for (int i = 0; i < count; ++i) {
     LinProblem& p = args.p[i];
-    if (!lin_operand(&tm[2 * i], &p.a_3d, L[i].A, L[i].a_mn, L[i].M, L[i].K, 128, L[i].lda) ||
-        !lin_operand(&tm[2 * i + 1], &p.b_3d, L[i].B, L[i].b_mn, L[i].N, L[i].K, plan[i].bn / 2, L[i].ldb))
+    if (!lin_operand(&maps.three[2 * i], &maps.two[2 * i], &p.a_whole, L[i].A, L[i].a_mn, L[i].M, L[i].K, 128,
+                     L[i].lda) ||
+        !lin_operand(&maps.three[2 * i + 1], &maps.two[2 * i + 1], &p.b_whole, L[i].B, L[i].b_mn, L[i].N, L[i].K,
+                     plan[i].bn / 2, L[i].ldb))
       return cudaErrorInvalidValue;
-    auto rows32 = [](const void* at, long long ld, int size) {
-      return at == nullptr || (ld * size % 32 == 0 && (reinterpret_cast<uintptr_t>(at) & 31u) == 0);
+    auto rows_of = [&](unsigned bytes) {
+      auto fits = [&](const void* at, long long ld, int size) {
+        return at == nullptr || (ld * size % bytes == 0 && reinterpret_cast<uintptr_t>(at) % bytes == 0);
+      };
+      return fits(p.e.y, p.e.ldy, p.e.y_f32 ? 4 : 2) && fits(p.e.z, p.e.ldz, 2) &&
+             fits(p.e.res, p.e.ldr, p.e.res_f32 ? 4 : 2);
     };
     p.M = L[i].M;
     p.N = L[i].N;
@@ -934,17 +1138,12 @@ cudaError_t launch_linear_gemm(const LinearProduct* L, int count, float* partial
     p.partial = partial;
     partial += lin_partial(plan[i]);
     p.e = L[i].e;
-    p.wide = rows32(p.e.y, p.e.ldy, p.e.y_f32 ? 4 : 2) && rows32(p.e.z, p.e.ldz, 2) &&
-             rows32(p.e.res, p.e.ldr, p.e.res_f32 ? 4 : 2);
+    p.wide = rows_of(32) ? 2 : rows_of(16) ? 1 : 0;
     items += static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits;
     if (items > (1ll << 30)) return cudaErrorInvalidValue;
     args.end[i] = static_cast<int>(items);
   }
-  if (count == 1) {
-    tm[2] = tm[0];
-    tm[3] = tm[1];
-    args.end[1] = args.end[0];
-  }
+  if (count == 1) args.end[1] = args.end[0];
   int bn = 32;
   for (int i = 0; i < count; ++i)
     if (plan[i].bn > bn) bn = plan[i].bn;
@@ -964,7 +1163,7 @@ cudaError_t launch_linear_gemm(const LinearProduct* L, int count, float* partial
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel, tm[0], tm[1], tm[2], tm[3], args);
+  e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel, maps, args);
   for (int i = 0; i < count && e == cudaSuccess; ++i) {
     const LinProblem& p = args.p[i];
     if (p.splits == 1) continue;
