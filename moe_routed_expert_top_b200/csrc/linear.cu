@@ -275,27 +275,28 @@ __device__ __forceinline__ LinLane lin_lane(const __nv_bfloat16* row, int cols) 
   l.word = l.c1 != 0 && l.c1 < cols;
   return l;
 }
-// The lane's words of the block's rows 0 1, 2 3, ... (rows: `ld` apart from row0 on)
-__device__ __forceinline__ void lin_fetch_rows(const __nv_bfloat16* row0, long long ld, int rows, int cols,
-                                               uint32_t (&r)[16]) {
+// The lane's words of the block's rows 0 1, 2 3, ... (rows: `ld` apart from row0 on);
+// returns the first value of the lane's own row, which no word has where s is 1. (No
+// load waits for another here.)
+__device__ __forceinline__ uint16_t lin_fetch_rows(const __nv_bfloat16* row0, long long ld, int rows, int cols,
+                                                   uint32_t (&r)[16]) {
   const __nv_bfloat16* row = row0 + ((threadIdx.x & 31) >> 4) * ld;
 #pragma unroll
   for (int i = 0; i < 16; ++i, row += 2 * ld) {
     r[i] = 0u;
     if (2 * i + static_cast<int>((threadIdx.x & 31) >> 4) >= rows) continue;
     const LinLane l = lin_lane(row, cols);
-    if (l.word) {
+    if (l.word)
       r[i] = *reinterpret_cast<const uint32_t*>(row + l.c0);
-    } else {
-      const uint16_t* at = reinterpret_cast<const uint16_t*>(row);
-      if (l.c0 < cols) r[i] = at[l.c0];
-      if (l.c1 < cols) r[i] |= static_cast<uint32_t>(at[l.c1]) << 16;
-    }
+    else if (l.c0 < cols)
+      r[i] = *reinterpret_cast<const uint16_t*>(row + l.c0);
   }
+  const int own = threadIdx.x & 31;
+  return own < rows ? *reinterpret_cast<const uint16_t*>(row0 + own * ld) : static_cast<uint16_t>(0);
 }
 // v += the residual's block that lin_fetch_rows brought (a thread's v: its row's columns)
 __device__ __forceinline__ void lin_add_rows(const __nv_bfloat16* row0, long long ld, int cols, const uint32_t (&r)[16],
-                                             float* block, uint32_t (&v)[32]) {
+                                             uint16_t head, float* block, uint32_t (&v)[32]) {
   uint16_t* b = reinterpret_cast<uint16_t*>(block);
   const int up = (threadIdx.x & 31) >> 4;
   const __nv_bfloat16* row = row0 + up * ld;
@@ -304,9 +305,10 @@ __device__ __forceinline__ void lin_add_rows(const __nv_bfloat16* row0, long lon
   for (int i = 0; i < 16; ++i, row += 2 * ld) {
     const LinLane l = lin_lane(row, cols);
     b[(2 * i + up) * 34 + l.c0] = static_cast<uint16_t>(r[i]);
-    if (l.c1 < cols) b[(2 * i + up) * 34 + l.c1] = static_cast<uint16_t>(r[i] >> 16);
+    if (l.word) b[(2 * i + up) * 34 + l.c1] = static_cast<uint16_t>(r[i] >> 16);
   }
   __syncwarp();
+  b[(threadIdx.x & 31) * 34] = head;
   uint32_t mine[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) mine[i] = reinterpret_cast<const uint32_t*>(block)[(threadIdx.x & 31) * 17 + i];
@@ -369,9 +371,10 @@ __device__ __forceinline__ void lin_rows_f32(float* row0, long long ld, int rows
     }
   }
 }
-// The epilogue of a block; `res` as lin_fetch_rows brought it.
+// The epilogue of a block; `res` and `head` as lin_fetch_rows brought them.
 __device__ __forceinline__ void lin_store_rows(const LinearEpilogue& e, long long m, int n, int rows, int cols,
-                                               uint32_t (&v)[32], const uint32_t (&res)[16], float* block) {
+                                               uint32_t (&v)[32], const uint32_t (&res)[16], uint16_t head,
+                                               float* block) {
   if (e.z != nullptr)
     lin_put_rows(static_cast<__nv_bfloat16*>(e.z) + m * e.ldz + n, e.ldz, rows, cols, v, block);
   lin_act32_of(e.act, v);
@@ -380,7 +383,8 @@ __device__ __forceinline__ void lin_store_rows(const LinearEpilogue& e, long lon
       lin_rows_f32<true>(const_cast<float*>(static_cast<const float*>(e.res)) + m * e.ldr + n, e.ldr, rows, cols, v,
                          block);
     else
-      lin_add_rows(static_cast<const __nv_bfloat16*>(e.res) + m * e.ldr + n, e.ldr, cols, res, block, v);
+      lin_add_rows(static_cast<const __nv_bfloat16*>(e.res) + m * e.ldr + n, e.ldr, cols, res, head,
+                   block, v);
   }
   if (e.y_f32)
     lin_rows_f32<false>(static_cast<float*>(e.y) + m * e.ldy + n, e.ldy, rows, cols, v, block);
@@ -597,13 +601,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         }
       __syncwarp();
       uint32_t res[16];
+      uint16_t head = 0;
       auto ask_res = [&](int j) {  // of the run at column j of the tile
         if (!fetch || j >= width) return;
         if (p.wide && width - j >= 32) {
           if (lane < rows) lin_fetch_res(p.e, m0 + lane, c0 + j, res, w32);
         } else {
-          lin_fetch_rows(static_cast<const __nv_bfloat16*>(p.e.res) + m0 * p.e.ldr + c0 + j, p.e.ldr, rows,
-                         min(32, width - j), res);
+          head = lin_fetch_rows(static_cast<const __nv_bfloat16*>(p.e.res) + m0 * p.e.ldr + c0 + j, p.e.ldr, rows,
+                                min(32, width - j), res);
         }
       };
       ask_res(grp * 32);
@@ -669,6 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           uint32_t now[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) now[i] = res[i];
+          const uint16_t now_head = head;
           ask_res(j + 64);
           if (has_bias) {
 #pragma unroll
@@ -683,7 +689,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           if (p.wide && cols == 32) {
             if (lane < rows) lin_store32(p.e, m0 + lane, n, v, now, w32);
           } else {
-            lin_store_rows(p.e, m0, n, rows, cols, v, now, block);
+            lin_store_rows(p.e, m0, n, rows, cols, v, now, now_head, block);
           }
         }
       }
