@@ -734,7 +734,13 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
   const bool near = p.wide && !p.e.y_f32 && (p.e.res == nullptr || !p.e.res_f32);
   if (!near) {
     const int width = min(pitch, N - n0);
-    float s[8] = {};
+    float s[8] = {}, bias[8], res[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = threadIdx.x + 32 * j;
+      bias[j] = c < width ? linear_bias(p.e, n0 + c) : 0.0f;
+      res[j] = c < width && p.e.res != nullptr ? linear_res(p.e, m, n0 + c) : 0.0f;
+    }
     for (int k0 = 0; k0 < p.splits; k0 += 4) {
       float v[4][8];
 #pragma unroll
@@ -752,7 +758,10 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = threadIdx.x + 32 * j;
-      if (c < width) linear_store(p.e, m, n0 + c, s[j]);
+      if (c >= width) continue;
+      float z;
+      const float y = linear_result(p.e, s[j], bias[j], res[j], &z);
+      linear_put(p.e, m, n0 + c, y, z);
     }
     return;
   }
