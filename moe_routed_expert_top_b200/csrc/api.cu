@@ -251,10 +251,11 @@ int linear_backward_products(const LinearShape& d, int which, moe::LinearProduct
   int count = 0;
   if (which & 1) {
     moe::LinearProduct& q = g[count++];
-    q.M = d.M;
-    q.N = d.K;
+    q.swap = d.M <= moe::kLinearSwapRows;
+    q.M = q.swap ? d.K : d.M;
+    q.N = q.swap ? d.M : d.K;
     q.K = d.N;
-    q.b_mn = 1;
+    (q.swap ? q.a_mn : q.b_mn) = 1;  // w
   }
   if (which & 2) {
     moe::LinearProduct& q = g[count++];
@@ -1152,11 +1153,11 @@ moe_status moe_linear_backward(const moe_linear_desc* desc, const void* dy, cons
   moe::LinearProduct g[2];
   const int count = linear_backward_products(d, (dx != nullptr ? 1 : 0) | (dw != nullptr ? 2 : 0), g);
   for (int i = 0; i < count; ++i) {
-    const bool first = i == 0 && dx != nullptr;
-    g[i].A = dz;
-    g[i].lda = lddz;
-    g[i].B = first ? w : x;
-    g[i].ldb = first ? d.ldw : d.ldx;
+    const bool first = i == 0 && dx != nullptr, swap = g[i].swap != 0;
+    g[i].A = swap ? w : dz;
+    g[i].lda = swap ? d.ldw : lddz;
+    g[i].B = swap ? dz : first ? w : x;
+    g[i].ldb = swap ? lddz : first ? d.ldw : d.ldx;
     g[i].e.y = first ? dx : dw;
     g[i].e.ldy = d.K;
   }

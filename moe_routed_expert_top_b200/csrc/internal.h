@@ -221,8 +221,8 @@ inline bool linear_is_few(int M, int N, int K) {
   return M <= kLinearFewRows || (M <= 32 && static_cast<long long>(N) * K <= (1ll << 24));
 }
 // Up to so many rows the tiles' rows are the weight's: 256 rows of the weight meet 32 to
-// 128 rows of x, where a tile of 256 rows of x would be mostly empty and its ring
-// hold fewer of the weight's bytes.
+// 128 rows of x (in the backward pass of dz), where a tile of 256 rows of x would be
+// mostly empty and its ring hold fewer of the weight's bytes.
 constexpr int kLinearSwapRows = 128;
 cudaError_t launch_linear_few(const LinearProduct& L, int32_t* status, cudaStream_t stream);
 // One or two products in one launch (count 1 or 2); partial: linear_gemm_partial()

@@ -1031,19 +1031,22 @@ struct LinPlan {
 
 // With a tile for every pair: whole tiles of 256 x 256. (An output that leaves part
 // of the last turn idle is no slower for it: the operands' way from L2 is shared
-// by all, and cutting the last turn's tiles along k measured the same.) With
-// fewer: the tiles are cut along k into parts of g blocks, or are 128 or 64 wide
-// (each product for itself), or both, whichever has the least modelled time in SM clocks: a 128-wide k block
-// takes about 800 + 2.4 bn, an item 3000 beside its blocks, and parts a second
-// kernel, their sums written, read and added. An fp32 result is made of parts of
-// at most 16 blocks (2048 k) throughout.
+// by all, and cutting the last turn's tiles along k, or tiles of 224 and 192 columns,
+// measured the same or worse.) But where one of two products has fewer tiles than
+// there are pairs, with items much longer than the other's (few rows: dx sums over
+// every column of y, dw over the rows), its tiles may be cut. With fewer tiles in
+// all: both products' are cut along k into parts of g blocks, or are 128 or 64 wide
+// (each product for itself), or both. Taken is whichever has the least modelled time
+// in SM clocks: a 128-wide k block takes about 800 + 2.4 bn, an item 3000 beside its
+// blocks, and parts a second kernel, their sums written, read and added. An fp32
+// result is made of parts of at most 16 blocks (2048 k) throughout.
 void lin_plan(const LinearProduct* L, int count, LinPlan* out) {
   const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
   double best = -1.0;
   for (int width = 0; width < (count == 2 ? 9 : 3); ++width) {
     LinPlan p[2] = {};
     int kb[2] = {0, 0}, kb_most = 0;
-    long long tiles = 0;
+    long long tiles = 0, of[2] = {0, 0};
     bool fp32 = false;
     for (int i = 0; i < count; ++i) {
       const int n32 = (L[i].N + 31) / 32 * 32, most = kMaxBn >> (i == 0 ? width % 3 : width / 3);
@@ -1051,12 +1054,18 @@ void lin_plan(const LinearProduct* L, int count, LinPlan* out) {
       p[i].tiles_m = (L[i].M + 255) / 256;
       p[i].tiles_n = (L[i].N + p[i].bn - 1) / p[i].bn;
       kb[i] = (L[i].K + kBk - 1) / kBk;
+      of[i] = static_cast<long long>(p[i].tiles_m) * p[i].tiles_n;
+      tiles += of[i];
       if (kb[i] > kb_most) kb_most = kb[i];
-      tiles += static_cast<long long>(p[i].tiles_m) * p[i].tiles_n;
       if (L[i].e.y_f32 && kb[i] > 16) fp32 = true;
     }
+    // the product that alone is cut, or -1: both
+    int alone = -1;
+    if (count == 2 && tiles >= pairs)
+      for (int i = 0; i < 2; ++i)
+        if (of[i] < pairs && kb[i] > 4 * kb[1 - i]) alone = i;
     const int least = fp32 ? (kb_most + 15) / 16 : 1;
-    const int most = tiles < pairs ? least + 31 : least;
+    const int most = tiles < pairs || alone >= 0 ? least + 31 : least;
     for (int cut = least; cut <= most; cut += 1 + cut / 8) {
       const int g = (kb_most + cut - 1) / cut;
       if (cut > least && g < 2) break;
@@ -1064,10 +1073,10 @@ void lin_plan(const LinearProduct* L, int count, LinPlan* out) {
       double bytes = 0.0, all = 0.0, longest = 0.0;
       LinPlan q[2] = {p[0], p[1]};
       for (int i = 0; i < count; ++i) {
-        q[i].splits = (kb[i] + g - 1) / g;
+        q[i].splits = alone >= 0 && alone != i ? 1 : (kb[i] + g - 1) / g;
         q[i].kb_split = (kb[i] + q[i].splits - 1) / q[i].splits;
         q[i].splits = (kb[i] + q[i].kb_split - 1) / q[i].kb_split;
-        const long long n = static_cast<long long>(q[i].tiles_m) * q[i].tiles_n * q[i].splits;
+        const long long n = of[i] * q[i].splits;
         const double one = q[i].kb_split * (800.0 + 2.4 * q[i].bn) + 3000.0;
         items += n;
         all += n * one;
