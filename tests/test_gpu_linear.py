@@ -104,6 +104,37 @@ def test_backward(i, shape):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("res_dt", [None, BF16, F32])
+@pytest.mark.parametrize("m,n,k,pad", [(300, 773, 200, 0), (257, 289, 1096, 1), (700, 260, 64, 3), (129, 520, 72, 4)])
+def test_rows_at_odd_addresses(m, n, k, pad, res_dt, out):
+    """Several tiles whose rows begin anywhere, their last columns single: y, z and the
+    residual each at another offset, and nothing written beside them."""
+    r = gen(m)
+    x, w, bias = r(m, k), r(n, k, sd=k ** -0.5), r(n)
+    res = None if res_dt is None else pitched(r(m, n, dt=res_dt), n + pad, 1)
+    L = Linear(w, bias, "gelu", out)
+    yp = pitched(torch.zeros(m, n, dtype=out, device=DEV), n + pad + 1, 3)
+    y, z = L.forward(x, residual=res, out=yp, with_z=True)
+    ref, tol, zr, dz = R.linear(x, w, bias, "gelu", res, out)
+    R.check(y, ref, tol, "y")
+    R.check(z, zr, dz + R.half(BF16) * (zr.abs() + dz), "z")
+    gap = yp.as_strided((m - 1, pad + 1), (n + pad + 1, 1), yp.storage_offset() + n)
+    assert gap.isnan().all()
+    if res_dt == out:  # y may be the residual
+        R.check(L.forward(x, residual=res, out=res), ref, tol, "in place")
+
+
+@pytest.mark.parametrize("m,n,k", [(20, 5000, 2056), (1, 4999, 2048), (128, 6001, 1048)])
+def test_backward_of_few_rows_and_a_wide_output(m, n, k):
+    """dx sums over many columns of y on few tiles, dw has many tiles of one block."""
+    r = gen(n)
+    x, w, dy = r(m, k), r(n, k, sd=k ** -0.5), r(m, n)
+    got = Linear(w, r(n)).backward(dy, x)
+    for what, g, (a, t) in zip(("dx", "dw", "dbias"), got, R.linear_backward(dy, x, w, None, "none")):
+        R.check(g, a, t, what)
+
+
 @pytest.mark.parametrize("name", ["none", "silu", "gelu"])
 def test_gradients_against_differences(name):
     """Inputs whose z is exact in bf16, so that the kernel's formula is that of the
