@@ -488,14 +488,15 @@ moe_status moe_experts_forward_few(const moe_problem* prob, const void* hidden, 
  * do not overlap, but y may be the residual (same pitch and type).
  * M, N >= 0 (0: no-op), K >= 1, K % 8 == 0, ldx % 8 == 0, ldw % 8 == 0, x and W
  * 16-byte aligned; y, z, bias and residual need only their type's alignment. Up to
- * MOE_LINEAR_FEW_ROWS rows run in a kernel that streams the weight, more on tcgen05 tiles.
+ * 8 rows run in a kernel that streams the weight, more, by the weight's size, there or on
+ * tcgen05 tiles.
  * Errors: MOE_ERR_INVALID_ARG for null, misaligned or negative arguments, a pitch
  * below its row, a bad act; MOE_ERR_UNSUPPORTED for K % 8, ldx % 8 or ldw % 8 and
  * for sizes above 2^24; MOE_ERR_WORKSPACE. `workspace` (32-byte aligned) holds the
  * device status word (its first int32, zeroed by the call; MOE_DEV_TIMEOUT) and
  * partial sums; calls whose work may overlap need one each. Up to
- * MOE_LINEAR_FEW_ROWS rows moe_linear has no partial sums and waits on nothing:
- * workspace may then be NULL (and no status is written).
+ * MOE_LINEAR_FEW_ROWS rows workspace may be NULL: the weight then streams, which
+ * has no partial sums and waits on nothing (and no status is written).
  * moe_linear_workspace_bytes returns 0 for a descriptor that moe_linear refuses. */
 #define MOE_LINEAR_FEW_ROWS 16
 enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };

@@ -238,7 +238,7 @@ int64_t linear_forward_bytes(const LinearShape& d) {
   if (moe::linear_is_few(d.M, d.N, d.K)) return 1024;
   if (d.N == 0) return 1024;
   const moe::LinearProduct g = linear_forward_product(d);
-  return 1024 + 4 * moe::linear_gemm_partial(&g, 1);
+  return 2048 + 4 * moe::linear_gemm_partial(&g, 1);  // (more than what streams needs)
 }
 
 struct LinearBackwardPlan {
@@ -1022,7 +1022,7 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
   moe_status s = check_linear(desc, &d);
   if (s != MOE_OK) return s;
   if (d.M == 0 || d.N == 0) return MOE_OK;
-  const bool few = moe::linear_is_few(d.M, d.N, d.K);
+  const bool few = moe::linear_is_few(d.M, d.N, d.K) || (workspace == nullptr && d.M <= moe::kLinearFewRows);
   if (x == nullptr || w == nullptr || y == nullptr ||
       (workspace == nullptr && d.M > moe::kLinearFewRows))
     return MOE_ERR_INVALID_ARG;

@@ -212,13 +212,18 @@ struct LinearProduct {
 };
 // Whether the weight streams through registers (linear_few.cu) or through the tiles
 // (linear.cu). The rows' words come from L1 for each tile of weight rows, so the
-// streaming kernel slows with the rows; the tiles cost more to begin and, with few
-// of them, a second kernel. Measured, streaming against tiles: 16384 x 7168 at 8 rows
-// 40 us, 16 rows 51 against 53, 17 rows 62 against 46, 32 rows 69 against 48; 4608 x 2048
-// at 17 rows 8 us against 12; 4096 x 4096 at 17 and 32 rows 13 and 14 against 13 and 14.5.
-constexpr int kLinearFewRows = 16;
+// streaming kernel slows with each 8 rows; the tiles cost more to begin and, with few
+// of them, a second kernel. Measured, streaming against tiles, us:
+//             8 rows       16 rows      17 rows      32 rows
+// 4608 x 2048   6.2  10.8    7.7  11.1    8.2  10.9    9.4  11.1
+// 4096 x 4096   9.2  13.3   11.1  13.7   12.4  13.6   13.8  14.0
+// 8192 x 4096  14.7  18.6   18.2  18.6   21.5  18.6   24.3  19.2
+// 7168 x 7168  21.2  24.5   26.0  24.8   31.6  24.9   35.4  25.2
+// 16384 x 7168 39.6  42.2   50.5  41.9   61.3  41.7   68.5  42.1
+constexpr int kLinearFewRows = 16;  // always may stream: needs no workspace
 inline bool linear_is_few(int M, int N, int K) {
-  return M <= kLinearFewRows || (M <= 32 && static_cast<long long>(N) * K <= (1ll << 24));
+  const long long size = static_cast<long long>(N) * K;
+  return M <= 8 || (M <= 16 && size <= (1ll << 25)) || (M <= 32 && size <= (1ll << 24));
 }
 // Up to so many rows the tiles' rows are the weight's: 256 rows of the weight meet 32 to
 // 128 rows of x (in the backward pass of dz), where a tile of 256 rows of x would be

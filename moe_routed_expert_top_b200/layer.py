@@ -372,8 +372,8 @@ class Linear:
             if out is None:
                 out = torch.empty(M, self.N, dtype=self.out_dtype, device=dev)
             z = torch.empty(M, self.N, dtype=torch.bfloat16, device=dev) if with_z else None
-            ws = None  # a few rows need none
-            if M > MOE_LINEAR_FEW_ROWS:
+            ws = None  # a few rows need none where the weight streams
+            if M > MOE_LINEAR_FEW_ROWS or need > 1024:
                 ws = torch.empty(need, dtype=torch.uint8, device=dev)
             self._ws = ws
             moe_linear(d, x, self.weight, self.bias, residual, out, z, ws, need, _stream_of(x))

@@ -125,6 +125,20 @@ def test_rows_at_odd_addresses(m, n, k, pad, res_dt, out):
         R.check(L.forward(x, residual=res, out=res), ref, tol, "in place")
 
 
+@pytest.mark.parametrize("m", [8, 9, 16])
+def test_few_rows_of_a_large_weight(m):
+    """With a workspace and without one: the weight on tiles and streamed."""
+    n, k = 5001, 8200
+    r = gen(m)
+    x, w, bias, res = r(m, k), r(n, k, sd=k ** -0.5), r(n), r(m, n)
+    ref, tol, _, _ = R.linear(x, w, bias, "silu", res, BF16)
+    R.check(Linear(w, bias, "silu").forward(x, residual=res), ref, tol, "layer")
+    d = M.make_linear_desc(m, n, k, "silu")
+    y = torch.full((m, n), torch.nan, dtype=BF16, device=DEV)
+    M.moe_linear(d, x, w, bias, res, y, None)
+    R.check(y, ref, tol, "no workspace")
+
+
 @pytest.mark.parametrize("m,n,k", [(20, 5000, 2056), (1, 4999, 2048), (128, 6001, 1048)])
 def test_backward_of_few_rows_and_a_wide_output(m, n, k):
     """dx sums over many columns of y on few tiles, dw has many tiles of one block."""
