@@ -15,7 +15,11 @@
 // behind it the tensor cores. A CTA pair (cluster of two on one TPC) computes a
 // 256 x 256 tile with 256-row MMAs (cta_group::2): each CTA fetches its 128 rows of A
 // and its half of B's rows, 64 KB a stage of 128 k against the 96 KB that a tile of
-// its own would take; the chip reads about 9.4 TB/s this way (measured at 8192^3).
+// its own would take; the chip reads about 9.4 TB/s this way (measured at 8192^3: 752
+// us, 1460 TFLOP/s; 4096 x 7168 x 2048 with silu and a residual 96 us, 1250 TFLOP/s; both
+// gradients of 4096 x 4096 x 7168 322 us, 1490 TFLOP/s). Rows that are no multiple of
+// 32 bytes cost every 128-byte piece a sector more: 4096 x 5120 x 2048 takes 68 us, with
+// a k of 2056 98.
 // Two accumulators in tensor memory let a tile's epilogue run under the next
 // one's main loop. Few tiles (a narrow output, few rows): k is split over the idle
 // pairs, each part leaves fp32 sums in the workspace and a second kernel adds them
@@ -262,7 +266,8 @@ __device__ __forceinline__ void lin_fetch_res(const LinearEpilogue& e, long long
 // block of 32 rows x `cols` columns goes through shared memory (17 words a row), so
 // that 16 lanes lie along a row: a lane has the columns s + 2w and s + 2w + 1, where s
 // is 1 in a row that begins between two words; in such a row lane 15 has the last
-// column and the first.
+// column and the first. (4096 x 5001 x 2048 72 us where 5120 columns take 68; a value an
+// access it was 158; with silu and a residual 118.)
 struct LinLane {
   int c0, c1;  // the lane's columns; whether they are one word
   bool word;
@@ -715,7 +720,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 // y of the tiles computed in parts: the parts' sums, in order. A block has 8 rows
 // of one tile, a thread 8 columns of one and the loads of 4 parts in flight. The
 // columns are neighbours where y's rows take 16-byte accesses, else 32 apart, so that
-// the lanes lie along the row.
+// the lanes lie along the row. (100 x 1001 x 2056 whole: 12.8 us, of 1024 columns 10.8.)
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinProblem p, int first) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tile = first + blockIdx.y;
@@ -826,7 +831,8 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 // unrounded values), and the column sums of a block's rows. A thread has V
 // columns, a block's 8 warps every eighth row. One pass, bound by HBM and by the
 // slope's arithmetic: a kernel for each activation, so that no branch parts a row's
-// values, and the loads of a warp's next rows together.
+// values, and the loads of a warp's next rows together (4096 x 4096 with gelu 22 us,
+// 4.6 TB/s).
 constexpr int kDzLines = 1024;  // blocks along M, at most
 template <int V, bool kF32, int kAct>
 __global__ void __launch_bounds__(256, 3) linear_dz_kernel(const LinearDzLaunch p) {

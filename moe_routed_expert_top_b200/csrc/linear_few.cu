@@ -8,7 +8,8 @@
 // warp is always 32 row pieces of 128 bytes; their shape follows the rows that a
 // CTA gets (kSpan): 32 rows x 64 k, 16 x 128 or 8 x 256. A router has 2 rows a
 // CTA: as 32 x 64 it would load 256 bytes a step and take k's length in memory
-// latencies.
+// latencies. Measured: 256 x 7168 at one row 4.8 us; 4096 x 4096 9 us at 1 to 8 rows, 13.8 at
+// 32; 16384 x 7168 at one row 38.6 us, 6.1 TB/s, 93% of the measured copy rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
