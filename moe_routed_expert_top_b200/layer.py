@@ -431,6 +431,7 @@ class LayerNorm:
         self.H = None if w is None else w.shape[0]
         self.device = None if w is None else w.device
         self.w_f32 = w is not None and w.dtype == torch.float32
+        self._needs = {}  # (M, H) -> workspace bytes of the backward pass
 
     def _check(self, x: torch.Tensor):
         if x.dim() != 2 or x.shape[1] < 1 or (self.H is not None and x.shape[1] != self.H):
@@ -465,15 +466,20 @@ class LayerNorm:
                     not t.is_contiguous():
                 raise ValueError(f"{name} must be a dense float32 vector of {M}")
         with _on_device_of(x):
-            dx = torch.empty(M, H, dtype=x.dtype, device=x.device) if need_dx else None
-            dw = db = ws = None
+            dx = dw = db = ws = None
+            need = 0
+            if need_dx:
+                dx = torch.empty_like(x, memory_format=torch.contiguous_format)
             if need_weights:
                 dw = torch.empty(H, dtype=torch.float32, device=x.device)
-                db = torch.empty(H, dtype=torch.float32, device=x.device)
-                ws = torch.empty(moe_layer_norm_backward_workspace_bytes(M, H), dtype=torch.uint8,
-                                 device=x.device)
+                db = torch.empty_like(dw)
+                need = self._needs.get((M, H))
+                if need is None:
+                    need = _remember(self._needs, (M, H),
+                                     moe_layer_norm_backward_workspace_bytes(M, H))
+                ws = torch.empty(need, dtype=torch.uint8, device=x.device)
             moe_layer_norm_backward(M, H, lddy, ldx, 0, x.dtype == torch.float32, self.w_f32, dy, x,
-                                    self.weight, mean, rstd, dx, dw, db, ws, None, _stream_of(x))
+                                    self.weight, mean, rstd, dx, dw, db, ws, need, _stream_of(x))
         return dx, dw, db
 
 
